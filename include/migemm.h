@@ -359,6 +359,101 @@ int gemm_debug_read(const migemm_plan* plan, const void* workspace, void* stream
 int gemm_run_no_alloc(const migemm_plan* plan, const void* A, const void* B, const void* C,
                       void* D, float alpha, float beta, void* stream);
 
+/*
+ * Operators around the product
+ * ============================
+ * What stands on either side of a GEMM in a large language model: the norm
+ * that makes its input, the product of 8-bit rows, and the loss over a large
+ * vocabulary.  Each has a description, a plan and runs, under the conventions
+ * at the top of this file; a plan of one kind is refused by the calls of
+ * another.  All matrices are row-major with a row stride *_rs in elements:
+ * at least the columns (else INVALID_ARG), a multiple of 16 bytes (else
+ * MISALIGNED), the matrix within 2^47 bytes (else UNSUPPORTED).  Base
+ * pointers are 16-byte aligned (vectors of fp32: 4-byte, where not said
+ * otherwise).  What lies between a row's columns and its stride is never
+ * written, and its contents do not matter.  Every run is a number of kernel
+ * launches on `stream`: it can be captured in a graph, gives the same bits on
+ * every call (no atomics decide an order of additions), and keeps nothing
+ * from one call for the next.  Workspaces need no initialization; calls that
+ * share one must not overlap in time.
+ */
+
+/* Norm: the residual's addition and the root-mean-square norm of each row.
+ *   h = bf16(x + r)                      (without a residual, h = x)
+ *   rstd = 1 / sqrt(mean of h^2 + eps)   (fp32)
+ *   y = bf16(h * rstd * weight), or, with y_type MIGEMM_FP8_E4M3,
+ *   scale = max |h * rstd * weight| / 448 and y = e4m3(h * rstd * weight /
+ *   scale), saturating at 448: the rows that gemm_scaled_run takes.  A row
+ *   of zeros gets scale 0 and codes 0; a NaN in a row makes its scale NaN.
+ * Gradients, with n = h * rstd and g = dy:
+ *   dx = bf16(rstd * (g * weight - n * mean(g * weight * n)) + dh)
+ *   dweight = sum over the rows of g * n  (fp32)
+ * (dx is the gradient of h: of both x and r.)  Sums are fp32: rows whose sum
+ * of squares passes 3e38 overflow.  cols is 1 .. 32768 (above: UNSUPPORTED);
+ * rows may be 0. */
+typedef struct migemm_norm_desc {
+  int64_t rows, cols;
+  int64_t x_rs, y_rs;        /* x: bf16; y: y_type */
+  int64_t r_rs, h_rs;        /* the residual in and out (bf16); both 0: none */
+  int64_t dy_rs, dx_rs;      /* backward pass (bf16); both 0: none */
+  int64_t dh_rs;             /* the residual's gradient (bf16); 0: none added */
+  float eps;                 /* > 0 and finite */
+  int32_t y_type;            /* MIGEMM_BF16 or MIGEMM_FP8_E4M3 */
+  int32_t device;            /* HIP device ordinal; must be gfx950 */
+  int32_t reserved;          /* must be 0 */
+} migemm_norm_desc;
+
+typedef struct migemm_norm_plan migemm_norm_plan; /* opaque, host memory only */
+
+int gemm_norm_desc_validate(const migemm_norm_desc* desc);
+int gemm_norm_plan_create(const migemm_norm_desc* desc, migemm_norm_plan** out);
+int gemm_norm_plan_destroy(migemm_norm_plan* plan);
+/* Bytes of workspace the backward pass needs (256-byte aligned): one row of
+ * fp32 column sums for each of the workgroups that walk the rows.  0 for a
+ * plan without a backward pass. */
+size_t gemm_norm_workspace_size(const migemm_norm_plan* plan);
+
+/* r and h are given exactly when the plan has a residual, scale (fp32 [rows])
+ * exactly when y is e4m3; rstd is fp32 [rows], weight bf16 [cols], 16-byte
+ * aligned.  h may be x or r itself (same strides), and a bf16 y may be x. */
+int gemm_norm_run(const migemm_norm_plan* plan, const void* x, const void* r, const void* weight,
+                  void* h, void* y, float* scale, float* rstd, void* stream);
+
+/* h is what the forward pass normed (stride h_rs with a residual, else x
+ * with stride x_rs), rstd what it wrote.  dh is given exactly when the plan
+ * has dh_rs.  dx may be dy or dh itself (same strides).  dweight is fp32
+ * [cols], written whole (zeros for no rows). */
+int gemm_norm_run_backward(const migemm_norm_plan* plan, const void* dy, const void* h,
+                           const void* weight, const float* rstd, const void* dh, void* dx,
+                           float* dweight, void* workspace, void* stream);
+
+/* The product of 8-bit rows, each with its scale, and 8-bit weights with a
+ * scale per output channel:
+ *   d[m][n] = bf16(a_scale[m] * b_scale[n] * sum over k of a[m][k] b[n][k])
+ * a is M x K and b N x K e4m3 (both K-contiguous: b_cs is the stride between
+ * the columns of the K x N operand), d M x N bf16; sums are fp32, rounded
+ * once.  From one row to many: the plan chooses among kernels by the sizes.
+ * M, N and K may be 0 (K = 0: d is zero); 256 rows of a, b and d each span
+ * less than 2^31 bytes (else UNSUPPORTED). */
+typedef struct migemm_scaled_desc {
+  int64_t M, N, K;
+  int64_t a_rs, b_cs, d_rs;
+  int32_t device;
+  int32_t reserved; /* must be 0 */
+} migemm_scaled_desc;
+
+typedef struct migemm_scaled_plan migemm_scaled_plan; /* opaque, host memory only */
+
+int gemm_scaled_desc_validate(const migemm_scaled_desc* desc);
+int gemm_scaled_plan_create(const migemm_scaled_desc* desc, migemm_scaled_plan** out);
+int gemm_scaled_plan_destroy(migemm_scaled_plan* plan);
+/* Bytes of workspace a run needs (256-byte aligned); 0: it may be NULL. */
+size_t gemm_scaled_workspace_size(const migemm_scaled_plan* plan);
+
+/* a_scale is fp32 [M], b_scale fp32 [N], both 16-byte aligned. */
+int gemm_scaled_run(const migemm_scaled_plan* plan, const void* a, const float* a_scale,
+                    const void* b, const float* b_scale, void* d, void* workspace, void* stream);
+
 /* Static text for a status code (never NULL).  No counterpart on the pages. */
 const char* gemm_status_string(int status);
 

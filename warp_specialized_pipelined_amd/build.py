@@ -19,6 +19,10 @@ LIB = os.path.join(HERE, "libmigemm.so")
 ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "gemm_kernels.hip")]
+# The operators around the product: their C ABI layer and kernel units.
+OPERATORS = os.path.join(CSRC, "operators")
+OPERATOR_API = os.path.join(OPERATORS, "operators_api.cpp")
+OPERATOR_KERNELS = ["norm_kernels", "scaled_kernels"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -61,21 +65,28 @@ def _obj(name):
 
 def build(verbose: bool = False, asan: bool = True) -> str:
     """Compile every HIP source into libmigemm.so (always recompiles): the
-    kernel translation unit once into an object, the C ABI layer, and the
-    link.  With asan, also _build/libmigemm_asan.so: the same kernel object
-    with the C ABI layer built under the host AddressSanitizer."""
-    kobj, aobj = _obj("gemm_kernels.o"), _obj("api.o")
-    _run([hipcc(), *HIPCC_FLAGS, "-c", "-o", kobj, os.path.join(CSRC, "gemm_kernels.hip")], verbose)
-    _run([hipcc(), *HIPCC_FLAGS, "-c", "-o", aobj, os.path.join(CSRC, "api.cpp")], verbose)
+    kernel translation units once into objects, the C ABI layers, and the
+    link.  With asan, also _build/libmigemm_asan.so: the same kernel objects
+    with the C ABI layers built under the host AddressSanitizer."""
+    from concurrent.futures import ThreadPoolExecutor
+    kernels = {_obj("gemm_kernels.o"): os.path.join(CSRC, "gemm_kernels.hip")}
+    kernels.update({_obj(n + ".o"): os.path.join(OPERATORS, n + ".hip") for n in OPERATOR_KERNELS})
+    api = {_obj("api.o"): SOURCES[0], _obj("operators_api.o"): OPERATOR_API}
+    jobs = [[hipcc(), *HIPCC_FLAGS, "-c", "-o", o, src] for o, src in {**kernels, **api}.items()]
+    sapi = []
+    if asan:
+        for o, src in list(api.items()):
+            sapi.append(o[:-2] + "_asan.o")
+            jobs.append([hipcc(), *HIPCC_FLAGS, *ASAN_HOST_FLAGS, "-c", "-o", sapi[-1], src])
+    with ThreadPoolExecutor(4) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
     tmp = LIB + ".tmp%d" % os.getpid()
-    _run([hipcc(), *HIPCC_FLAGS, "-shared", "-o", tmp, aobj, kobj], verbose)
+    _run([hipcc(), *HIPCC_FLAGS, "-shared", "-o", tmp, *api, *kernels], verbose)
     os.replace(tmp, LIB)
     if asan:
-        sobj, slib = _obj("api_asan.o"), _obj("libmigemm_asan.so")
-        _run([hipcc(), *HIPCC_FLAGS, *ASAN_HOST_FLAGS, "-c", "-o", sobj,
-              os.path.join(CSRC, "api.cpp")], verbose)
-        _run([hipcc(), *HIPCC_FLAGS, *ASAN_HOST_FLAGS, "-shared", "-o", slib + ".tmp", sobj, kobj],
-             verbose)
+        slib = _obj("libmigemm_asan.so")
+        _run([hipcc(), *HIPCC_FLAGS, *ASAN_HOST_FLAGS, "-shared", "-o", slib + ".tmp", *sapi,
+              *kernels], verbose)
         os.replace(slib + ".tmp", slib)
     return LIB
 
@@ -120,12 +131,12 @@ def build_c_client(verbose: bool = False) -> list:
     return built
 
 
-def dump_asm(out_dir: str) -> str:
-    """Write the gfx950 assembly of the kernel translation unit to out_dir."""
+def dump_asm(out_dir: str, unit: str = "gemm_kernels") -> str:
+    """Write the gfx950 assembly of a kernel translation unit to out_dir."""
     os.makedirs(out_dir, exist_ok=True)
-    out = os.path.join(out_dir, "gemm_kernels.s")
+    out = os.path.join(out_dir, unit + ".s")
     cmd = [hipcc(), *HIPCC_FLAGS, "--cuda-device-only", "-S", "-o", out,
-           os.path.join(CSRC, "gemm_kernels.hip")]
+           os.path.join(OPERATORS if unit in OPERATOR_KERNELS else CSRC, unit + ".hip")]
     subprocess.run(cmd, check=True, cwd=CSRC)
     return out
 

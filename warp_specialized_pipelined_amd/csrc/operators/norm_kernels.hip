@@ -1,0 +1,385 @@
+// norm_kernels.hip -- the residual's addition and the root-mean-square norm
+// of each row, with bf16 or e4m3 output, and its gradient.
+//
+// Forward, per row of n columns:
+//   h = bf16(x + r)                       (h = x without a residual)
+//   rstd = 1 / sqrt(sum h^2 / n + eps)    (fp32 sum)
+//   bf16:  y = bf16(h rstd w)
+//   e4m3:  top = max |h w|;  scale = top rstd / 448;  y = e4m3(h w 448 / top)
+// The e4m3 codes do not need rstd (it cancels: y / scale = h w 448 / top), so
+// the sum and the maximum come out of one pass over registers and one
+// reduction.
+//
+// Backward, with n = h rstd and g = dy:
+//   dx = rstd (g w - n mean(g w n)) + dh,   dweight = sum over rows of g n
+//
+// Bound: memory (6 to 14 bytes an element).  A row is read once, 16 bytes a
+// lane, and stays in registers between the reduction and the output.
+#include <hip/hip_runtime.h>
+
+#include "../kernel/gfx950.hpp"
+#include "operators.h"
+
+namespace migemm {
+namespace {
+
+constexpr float kE4M3Max = 448.0f;
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+// Maximum of non-negative floats (and NaN) as unsigned bit patterns: a NaN's
+// pattern is above infinity's, so it wins.
+__device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t o = __shfl_xor(v, d, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// Eight consecutive bf16 of a row at column c.  The row starts on a 16-byte
+// boundary, so a vector that holds the last columns may be read whole (the
+// bytes past them share its 16-byte block); what lies past the columns is
+// replaced by zeros.
+__device__ __forceinline__ u32x4 load8(const unsigned short* row, int64_t c, int64_t cols) {
+  u32x4 v = {0, 0, 0, 0};
+  if (c < cols) {
+    v = *reinterpret_cast<const u32x4*>(row + c);
+    const int left = cols - c < 8 ? (int)(cols - c) : 8;
+    if (left < 8) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        v[w] = 2 * w + 2 <= left ? v[w] : (2 * w + 1 == left ? v[w] & 0xFFFFu : 0u);
+    }
+  }
+  return v;
+}
+__device__ __forceinline__ void store8(unsigned short* row, int64_t c, int64_t cols, u32x4 v) {
+  if (c + 8 <= cols) {
+    *reinterpret_cast<u32x4*>(row + c) = v;
+  } else if (c < cols) {
+    for (int e = 0; e < (int)(cols - c); ++e)
+      row[c + e] = (unsigned short)(v[e >> 1] >> (16 * (e & 1)));
+  }
+}
+__device__ __forceinline__ float lo(uint32_t w) { return bf16_lo(w); }
+__device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
+
+// Past +-448 (by rounding only: |v| <= 448 (1 + 2^-23)) the value is 448;
+// a NaN stays one.
+__device__ __forceinline__ float clamp448(float v) {
+  return fabsf(v) > kE4M3Max ? copysignf(kE4M3Max, v) : v;
+}
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(a), clamp448(b), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(clamp448(c), clamp448(d), w, true);
+}
+
+constexpr int threads_of(int waves) { return waves == 1 ? 256 : 64 * waves; }
+constexpr int rows_of(int waves) { return waves == 1 ? 4 : 1; }
+
+// WAVES waves share a row (with one, a workgroup takes 4 rows), NV vectors
+// of 8 columns each lane.
+template <int WAVES, int NV, bool RES, bool E4M3>
+__device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int t, int wave, int lane,
+                                         int phase) {
+  constexpr int kLanes = 64 * WAVES;
+  const unsigned short* x = static_cast<const unsigned short*>(a.x) + row * a.x_rs;
+  const unsigned short* w = static_cast<const unsigned short*>(a.weight);
+
+  u32x4 hv[NV], wv[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) hv[i] = load8(x, (int64_t)(i * kLanes + t) * 8, a.cols);
+  if constexpr (RES) {
+    const unsigned short* r = static_cast<const unsigned short*>(a.r) + row * a.r_rs;
+    u32x4 rv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) rv[i] = load8(r, (int64_t)(i * kLanes + t) * 8, a.cols);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) wv[i] = load8(w, (int64_t)(i * kLanes + t) * 8, a.cols);
+    unsigned short* h = static_cast<unsigned short*>(a.h) + row * a.h_rs;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        hv[i][q] = pack_bf16x2(lo(hv[i][q]) + lo(rv[i][q]), hi(hv[i][q]) + hi(rv[i][q]));
+      store8(h, (int64_t)(i * kLanes + t) * 8, a.cols, hv[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) wv[i] = load8(w, (int64_t)(i * kLanes + t) * 8, a.cols);
+  }
+
+  float sum = 0.0f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float h0 = lo(hv[i][q]), h1 = hi(hv[i][q]);
+      sum += h0 * h0;
+      sum += h1 * h1;
+      if constexpr (E4M3) {
+        const uint32_t b0 = __float_as_uint(h0 * lo(wv[i][q])) & 0x7FFFFFFFu;
+        const uint32_t b1 = __float_as_uint(h1 * hi(wv[i][q])) & 0x7FFFFFFFu;
+        top = b0 > top ? b0 : top;
+        top = b1 > top ? b1 : top;
+      }
+    }
+  sum = wave_sum(sum);
+  if constexpr (E4M3) top = wave_max_bits(top);
+  if constexpr (WAVES > 1) {
+    // Two buffers: a wave that is already at its next row writes the other
+    // one, and cannot come round to this one before the barrier between.
+    __shared__ float sums[2][WAVES];
+    __shared__ uint32_t tops[2][WAVES];
+    if (lane == 0) {
+      sums[phase][wave] = sum;
+      tops[phase][wave] = top;
+    }
+    __syncthreads();
+    sum = 0.0f;
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      sum += sums[phase][i];
+      top = tops[phase][i] > top ? tops[phase][i] : top;
+    }
+  }
+  const float rstd = rsqrtf(sum / (float)a.cols + a.eps);
+  if (t == 0) a.rstd[row] = rstd;
+
+  if constexpr (E4M3) {
+    const float largest = __uint_as_float(top);
+    if (t == 0) a.scale[row] = largest * rstd / kE4M3Max;
+    // Rows of values so small that 448 / largest would overflow are lifted.
+    const float lift = largest < 0x1p-96f ? 0x1p96f : 1.0f;
+    const float inv = largest == 0.0f ? 0.0f : kE4M3Max / (largest * lift);
+    unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.y_rs;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * kLanes + t) * 8;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = lo(hv[i][q]) * lo(wv[i][q]) * lift * inv;
+        v[2 * q + 1] = hi(hv[i][q]) * hi(wv[i][q]) * lift * inv;
+      }
+      const u32x2 o = {pack_e4m3x4(v[0], v[1], v[2], v[3]), pack_e4m3x4(v[4], v[5], v[6], v[7])};
+      if (c + 8 <= a.cols) {
+        *reinterpret_cast<u32x2*>(y + c) = o;
+      } else if (c < a.cols) {
+        for (int e = 0; e < (int)(a.cols - c); ++e) y[c + e] = (unsigned char)(o[e >> 2] >> (8 * (e & 3)));
+      }
+    }
+  } else {
+    unsigned short* y = static_cast<unsigned short*>(a.y) + row * a.y_rs;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      u32x4 o;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o[q] = pack_bf16x2(lo(hv[i][q]) * rstd * lo(wv[i][q]), hi(hv[i][q]) * rstd * hi(wv[i][q]));
+      store8(y, (int64_t)(i * kLanes + t) * 8, a.cols, o);
+    }
+  }
+}
+
+template <int WAVES, int NV, bool RES, bool E4M3>
+__global__ __launch_bounds__(threads_of(WAVES)) void norm_forward(NormArgs a) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int t = WAVES == 1 ? lane : (int)threadIdx.x;
+  // One row, unless the grid is at its cap (launch_norm_forward).
+  int phase = 0;
+  const int64_t step = (int64_t)gridDim.x * rows_of(WAVES);
+  for (int64_t row = (int64_t)blockIdx.x * rows_of(WAVES) + (WAVES == 1 ? wave : 0); row < a.rows;
+       row += step, phase ^= 1)
+    norm_row<WAVES, NV, RES, E4M3>(a, row, t, wave, lane, phase);
+}
+
+// Each walker (a workgroup, or with WAVES = 1 a wave) takes rows walker,
+// walker + walkers, ... and keeps its columns' sums of g n in registers; the
+// sums go to the walker's row of the workspace, and norm_sum_partials adds
+// those rows in a fixed order: no atomics, the same result on every run.
+template <int WAVES, int NV, bool RES>
+__global__ __launch_bounds__(threads_of(WAVES)) void norm_backward(NormArgs a) {
+  constexpr int kLanes = 64 * WAVES;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t walker = (int64_t)blockIdx.x * rows_of(WAVES) + (WAVES == 1 ? wave : 0);
+  if (walker >= a.partial_rows) return;
+  const int t = WAVES == 1 ? lane : (int)threadIdx.x;
+  const unsigned short* w = static_cast<const unsigned short*>(a.weight);
+  const float cols = (float)a.cols;
+
+  u32x4 wv[NV];
+  float dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    wv[i] = load8(w, (int64_t)(i * kLanes + t) * 8, a.cols);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  }
+  __shared__ float sums[2][WAVES];
+  int phase = 0;
+  for (int64_t row = walker; row < a.rows; row += a.partial_rows) {
+    const unsigned short* g = static_cast<const unsigned short*>(a.dy) + row * a.dy_rs;
+    const unsigned short* h = static_cast<const unsigned short*>(a.x) + row * a.x_rs;
+    u32x4 gv[NV], hv[NV], dhv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) gv[i] = load8(g, (int64_t)(i * kLanes + t) * 8, a.cols);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) hv[i] = load8(h, (int64_t)(i * kLanes + t) * 8, a.cols);
+    if constexpr (RES) {
+      const unsigned short* dh = static_cast<const unsigned short*>(a.dh) + row * a.dh_rs;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dhv[i] = load8(dh, (int64_t)(i * kLanes + t) * 8, a.cols);
+    }
+    const float rstd = a.rstd[row];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float n0 = lo(hv[i][q]) * rstd, n1 = hi(hv[i][q]) * rstd;
+        const float g0 = lo(gv[i][q]), g1 = hi(gv[i][q]);
+        dw[i][2 * q] += g0 * n0;
+        dw[i][2 * q + 1] += g1 * n1;
+        s += g0 * lo(wv[i][q]) * n0;
+        s += g1 * hi(wv[i][q]) * n1;
+      }
+    s = wave_sum(s);
+    if constexpr (WAVES > 1) {
+      // (Two buffers, as in the forward pass.)
+      if (lane == 0) sums[phase][wave] = s;
+      __syncthreads();
+      s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) s += sums[phase][i];
+      phase ^= 1;
+    }
+    const float mean = s / cols;
+    unsigned short* dx = static_cast<unsigned short*>(a.dx) + row * a.dx_rs;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      u32x4 o;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float n0 = lo(hv[i][q]) * rstd, n1 = hi(hv[i][q]) * rstd;
+        float d0 = rstd * (lo(gv[i][q]) * lo(wv[i][q]) - n0 * mean);
+        float d1 = rstd * (hi(gv[i][q]) * hi(wv[i][q]) - n1 * mean);
+        if constexpr (RES) {
+          d0 += lo(dhv[i][q]);
+          d1 += hi(dhv[i][q]);
+        }
+        o[q] = pack_bf16x2(d0, d1);
+      }
+      store8(dx, (int64_t)(i * kLanes + t) * 8, a.cols, o);
+    }
+  }
+  float* p = a.partials + walker * a.cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)(i * kLanes + t) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < a.cols) p[c + e] = dw[i][e];
+  }
+}
+
+// dweight[c] = sum over partial rows, 32 columns a workgroup: 32 threads a
+// column add every 32nd row, then one adds the 32 sums in order.
+__global__ __launch_bounds__(1024) void norm_sum_partials(NormArgs a) {
+  __shared__ float part[32][33];
+  const int col = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+  float s = 0.0f;
+  if (c < a.cols)
+    for (int64_t p = group; p < a.partial_rows; p += 32) s += a.partials[p * a.cols + c];
+  part[group][col] = s;
+  __syncthreads();
+  if (group == 0 && c < a.cols) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += part[i][col];
+    a.dweight[c] = s;
+  }
+}
+
+typedef void (*norm_fn)(NormArgs);
+
+template <int WAVES, int NV>
+norm_fn forward_of(bool res, bool e4m3) {
+  if (res) return e4m3 ? norm_forward<WAVES, NV, true, true> : norm_forward<WAVES, NV, true, false>;
+  return e4m3 ? norm_forward<WAVES, NV, false, true> : norm_forward<WAVES, NV, false, false>;
+}
+template <int WAVES>
+norm_fn forward_pick(int nv, bool res, bool e4m3) {
+  return nv == 1 ? forward_of<WAVES, 1>(res, e4m3)
+                 : (nv == 2 ? forward_of<WAVES, 2>(res, e4m3) : forward_of<WAVES, 4>(res, e4m3));
+}
+template <int WAVES>
+norm_fn backward_pick(int nv, bool res) {
+  if (res) return nv == 1 ? norm_backward<WAVES, 1, true>
+                          : (nv == 2 ? norm_backward<WAVES, 2, true> : norm_backward<WAVES, 4, true>);
+  return nv == 1 ? norm_backward<WAVES, 1, false>
+                 : (nv == 2 ? norm_backward<WAVES, 2, false> : norm_backward<WAVES, 4, false>);
+}
+
+// The fewest waves from `waves` on (1, 4, 16) whose lanes hold the row in
+// `most` vectors, and the vectors that takes.
+NormShape shape_for(int64_t cols, int waves, int most) {
+  while (waves < 16 && (int64_t)waves * 512 * most < cols) waves *= 4;
+  const int64_t v = (cols + waves * 512 - 1) / (waves * 512);
+  return {waves, v <= 1 ? 1 : (v <= 2 ? 2 : 4)};
+}
+
+}  // namespace
+
+NormShape norm_forward_shape(int64_t rows, int64_t cols) {
+  (void)rows;
+  return shape_for(cols, 1, cols <= 1024 ? 2 : 4);
+}
+NormShape norm_backward_shape(int64_t rows, int64_t cols) {
+  (void)rows;
+  return shape_for(cols, 1, cols <= 1024 ? 2 : 4);
+}
+
+int64_t norm_partial_rows(int64_t rows, int64_t cols, int cu_count) {
+  const NormShape s = norm_backward_shape(rows, cols);
+  const int64_t walkers = (int64_t)cu_count * 2 * rows_of(s.waves);
+  return rows < walkers ? rows : walkers;
+}
+
+hipError_t launch_norm_forward(const NormArgs& a, bool e4m3, hipStream_t stream) {
+  const NormShape s = norm_forward_shape(a.rows, a.cols);
+  const bool res = a.r != nullptr;
+  const norm_fn f = s.waves == 1 ? forward_pick<1>(s.vectors, res, e4m3)
+                                 : (s.waves == 4 ? forward_pick<4>(s.vectors, res, e4m3)
+                                                 : forward_pick<16>(s.vectors, res, e4m3));
+  int64_t grid = (a.rows + rows_of(s.waves) - 1) / rows_of(s.waves);
+  if (grid > (1 << 20)) grid = 1 << 20;  // a launch holds fewer than 2^32 threads
+  hipLaunchKernelGGL(f, dim3((uint32_t)grid), dim3(threads_of(s.waves)), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream) {
+  const NormShape s = norm_backward_shape(a.rows, a.cols);
+  const bool res = a.dh != nullptr;
+  if (a.partial_rows > 0) {
+    const norm_fn f = s.waves == 1 ? backward_pick<1>(s.vectors, res)
+                                   : (s.waves == 4 ? backward_pick<4>(s.vectors, res)
+                                                   : backward_pick<16>(s.vectors, res));
+    const int64_t grid = (a.partial_rows + rows_of(s.waves) - 1) / rows_of(s.waves);
+    hipLaunchKernelGGL(f, dim3((uint32_t)grid), dim3(threads_of(s.waves)), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(norm_sum_partials, dim3((uint32_t)((a.cols + 31) / 32)), dim3(1024), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace migemm

@@ -1,0 +1,63 @@
+// operators.h -- internal interface between the operators' plan layer
+// (operators_api.cpp) and their kernels: argument blocks and launches.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../kernel/params.hpp"
+
+namespace migemm {
+
+// ------------------------------------------------------------------- norm
+
+struct NormArgs {
+  const void* x;        // forward: bf16 input; backward: h, the normed input
+  const void* r;        // forward: residual in (NULL: none)
+  const void* dy;       // backward
+  const void* dh;       // backward: the residual's gradient (NULL: none)
+  const void* weight;   // bf16 [cols]
+  void* h;              // forward: residual out
+  void* y;              // forward: bf16 or e4m3
+  void* dx;             // backward
+  float* scale;         // forward, e4m3
+  float* rstd;          // forward: out; backward: in
+  float* dweight;       // backward
+  float* partials;      // backward: workspace, one row of cols sums per row walker
+  int64_t rows, cols;
+  int64_t x_rs, r_rs, h_rs, y_rs, dy_rs, dh_rs, dx_rs;  // elements
+  int64_t partial_rows;
+  float eps;
+};
+
+// Widest row the kernels hold in registers.
+constexpr int64_t kNormMaxCols = 16 * 64 * 4 * 8;
+
+// How a row is shared out: waves per row (1, 4 or 16) and 16-byte vectors
+// per lane (1, 2 or 4).
+struct NormShape {
+  int waves, vectors;
+};
+NormShape norm_forward_shape(int64_t rows, int64_t cols);
+NormShape norm_backward_shape(int64_t rows, int64_t cols);
+// Rows of partial column sums the backward pass leaves in its workspace.
+int64_t norm_partial_rows(int64_t rows, int64_t cols, int cu_count);
+
+hipError_t launch_norm_forward(const NormArgs& a, bool e4m3, hipStream_t stream);
+hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream);
+
+// ----------------------------------------------------------------- scaled
+
+struct ScaledArgs {
+  KernelArgs gemm;       // A, B: e4m3, K-contiguous; strides in elements
+  const float* a_scale;  // [M]
+  const float* b_scale;  // [N], 16-byte aligned
+};
+
+// Which kernel takes a product: 0 for 256 x 256 tiles, else a variant of the
+// small tiles.
+int scaled_variant(int64_t M, int64_t N, int64_t K, int cu_count);
+hipError_t prepare_scaled();
+hipError_t launch_scaled(const ScaledArgs& a, int variant, int grid, hipStream_t stream);
+
+}  // namespace migemm

@@ -1,0 +1,294 @@
+// operators_api.cpp -- the C ABI of the operators around the product
+// (include/migemm.h): description checks, plans and run entry points.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <new>
+#include <unordered_map>
+
+#include "../../../include/migemm.h"
+#include "operators.h"
+
+struct migemm_scaled_plan {
+  migemm_scaled_desc desc;
+  migemm::ScaledArgs base;  // the shape's part of the kernel arguments
+  int variant, grid;
+};
+
+struct migemm_norm_plan {
+  migemm_norm_desc desc;
+  int64_t partial_rows;
+  size_t workspace_bytes;
+};
+
+namespace {
+
+constexpr int64_t kMaxSpanBytes = (int64_t)1 << 47;
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// A row-major rows x cols matrix with row stride rs: rs covers the columns
+// (INVALID_ARG), starts every row on 16 bytes (MISALIGNED), and the matrix
+// stays within 2^47 bytes (UNSUPPORTED), which keeps every later product of
+// sizes and strides far from overflow.
+int check_matrix(int64_t rows, int64_t cols, int64_t rs, int es) {
+  if (rs < (cols > 1 ? cols : 1)) return MIGEMM_ERR_INVALID_ARG;
+  if (rs % (16 / es) != 0) return MIGEMM_ERR_MISALIGNED;
+  if (rows > kMaxSpanBytes || cols > kMaxSpanBytes || rs > kMaxSpanBytes) return MIGEMM_ERR_UNSUPPORTED;
+  if ((__int128)rows * rs * es > kMaxSpanBytes) return MIGEMM_ERR_UNSUPPORTED;
+  return MIGEMM_OK;
+}
+
+int check_device(int32_t device, int* cu_count) {
+  int count = 0;
+  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) return MIGEMM_ERR_DEVICE;
+  if (device < 0 || device >= count) return MIGEMM_ERR_DEVICE;
+  hipDeviceProp_t prop;
+  if (hipGetDeviceProperties(&prop, device) != hipSuccess) return MIGEMM_ERR_DEVICE;
+  if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return MIGEMM_ERR_DEVICE;
+  *cu_count = prop.multiProcessorCount;
+  return MIGEMM_OK;
+}
+
+bool current_device_is(int32_t device) {
+  int cur = -1;
+  return hipGetDevice(&cur) == hipSuccess && cur == device;
+}
+
+// The operators' plans alive in this process, by kind, so that a destroyed
+// plan or any other pointer is refused unread.  (Never freed, so that plans
+// destroyed while the process exits still find it.)
+enum PlanKind { kNorm = 1, kScaled = 2, kVocabLoss = 3 };
+std::mutex g_mu;
+std::unordered_map<const void*, PlanKind>& live() {
+  static auto* m = new std::unordered_map<const void*, PlanKind>();
+  return *m;
+}
+bool is_live(const void* p, PlanKind kind) try {
+  if (!p) return false;
+  std::lock_guard<std::mutex> lock(g_mu);
+  auto it = live().find(p);
+  return it != live().end() && it->second == kind;
+} catch (...) {
+  return false;
+}
+template <class Plan>
+int add_live(Plan* p, PlanKind kind, Plan** out) {
+  try {
+    std::lock_guard<std::mutex> lock(g_mu);
+    live()[p] = kind;
+  } catch (...) {  // no memory for the entry: no exception leaves a C entry point
+    delete p;
+    return MIGEMM_ERR_INVALID_ARG;
+  }
+  *out = p;
+  return MIGEMM_OK;
+}
+template <class Plan>
+int destroy(Plan* p, PlanKind kind) try {
+  if (!p) return MIGEMM_OK;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    auto it = live().find(p);
+    if (it == live().end() || it->second != kind) return MIGEMM_ERR_INVALID_ARG;
+    live().erase(it);
+  }
+  delete p;
+  return MIGEMM_OK;
+} catch (...) {
+  return MIGEMM_ERR_INVALID_ARG;
+}
+
+int launched(hipError_t e) { return e == hipSuccess ? MIGEMM_OK : MIGEMM_ERR_LAUNCH; }
+
+int check_workspace(size_t bytes, const void* workspace) {
+  if (bytes == 0) return MIGEMM_OK;
+  if (!workspace) return MIGEMM_ERR_INVALID_ARG;
+  return aligned(workspace, 256) ? MIGEMM_OK : MIGEMM_ERR_MISALIGNED;
+}
+
+// The 256 x 256 tiles of an M x N product and their order, as the GEMM's plan
+// lays them out.
+void set_tiles(migemm::KernelArgs& a) {
+  a.tiles_m = (int32_t)((a.M + migemm::kTileM - 1) / migemm::kTileM);
+  a.tiles_n = (int32_t)((a.N + migemm::kTileN - 1) / migemm::kTileN);
+  a.num_tiles = a.tiles_per_batch = a.tiles_m * a.tiles_n;
+  a.group_m = a.tiles_m < 8 ? (a.tiles_m > 0 ? a.tiles_m : 1) : 8;
+}
+
+// The kernels reach 256 rows of an operand with 32-bit offsets.
+constexpr int64_t kMaxBand = 0x7FFFFFF0 - 1024;
+bool band_fits(int64_t rs, int es) { return (__int128)256 * rs * es <= kMaxBand; }
+
+// Tile counts are 32-bit.
+bool tiles_fit(int64_t rows, int64_t cols) {
+  const __int128 t = ((__int128)rows / 16 + 1) * ((__int128)cols / 16 + 1);
+  return rows / 256 < (1 << 20) && cols / 256 < (1 << 20) && t < 0x7FFFFFFF;
+}
+
+// --------------------------------------------------------------------- norm
+
+bool norm_residual(const migemm_norm_desc& d) { return d.r_rs != 0; }
+bool norm_backward(const migemm_norm_desc& d) { return d.dx_rs != 0; }
+
+int validate_norm(const migemm_norm_desc* d) {
+  if (!d || d->rows < 0 || d->cols < 1 || d->reserved != 0) return MIGEMM_ERR_INVALID_ARG;
+  if (!(d->eps > 0.0f) || !std::isfinite(d->eps)) return MIGEMM_ERR_INVALID_ARG;
+  if (d->y_type != MIGEMM_BF16 && d->y_type != MIGEMM_FP8_E4M3) return MIGEMM_ERR_INVALID_ARG;
+  // The residual comes in and goes out, or neither; likewise the backward
+  // pass's operands; the residual's gradient needs a backward pass.
+  if ((d->r_rs != 0) != (d->h_rs != 0) || (d->dy_rs != 0) != (d->dx_rs != 0) ||
+      (d->dh_rs != 0 && d->dx_rs == 0))
+    return MIGEMM_ERR_INVALID_ARG;
+  const struct { int64_t rs; int es; bool used; } m[] = {
+      {d->x_rs, 2, true},
+      {d->y_rs, d->y_type == MIGEMM_BF16 ? 2 : 1, true},
+      {d->r_rs, 2, d->r_rs != 0}, {d->h_rs, 2, d->h_rs != 0}, {d->dy_rs, 2, d->dy_rs != 0},
+      {d->dh_rs, 2, d->dh_rs != 0}, {d->dx_rs, 2, d->dx_rs != 0}};
+  for (const auto& e : m) {
+    if (!e.used) continue;
+    const int st = check_matrix(d->rows, d->cols, e.rs, e.es);
+    if (st != MIGEMM_OK) return st;
+  }
+  return d->cols > migemm::kNormMaxCols ? MIGEMM_ERR_UNSUPPORTED : MIGEMM_OK;
+}
+
+// ------------------------------------------------------------------- scaled
+
+int validate_scaled(const migemm_scaled_desc* d) {
+  if (!d || d->M < 0 || d->N < 0 || d->K < 0 || d->reserved != 0) return MIGEMM_ERR_INVALID_ARG;
+  int st = check_matrix(d->M, d->K, d->a_rs, 1);
+  if (st == MIGEMM_OK) st = check_matrix(d->N, d->K, d->b_cs, 1);
+  if (st == MIGEMM_OK) st = check_matrix(d->M, d->N, d->d_rs, 2);
+  if (st != MIGEMM_OK) return st;
+  if (!band_fits(d->a_rs, 1) || !band_fits(d->b_cs, 1) || !band_fits(d->d_rs, 2) ||
+      !tiles_fit(d->M, d->N))
+    return MIGEMM_ERR_UNSUPPORTED;
+  return MIGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_scaled_desc_validate(const migemm_scaled_desc* desc) { return validate_scaled(desc); }
+
+int gemm_scaled_plan_create(const migemm_scaled_desc* desc, migemm_scaled_plan** out) {
+  if (!out) return MIGEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  int st = validate_scaled(desc);
+  if (st != MIGEMM_OK) return st;
+  int cus = 0;
+  st = check_device(desc->device, &cus);
+  if (st != MIGEMM_OK) return st;
+  if (migemm::prepare_scaled() != hipSuccess) return MIGEMM_ERR_DEVICE;
+  migemm_scaled_plan* p = new (std::nothrow) migemm_scaled_plan();
+  if (!p) return MIGEMM_ERR_INVALID_ARG;
+  p->desc = *desc;
+  migemm::KernelArgs& a = p->base.gemm;
+  a.M = desc->M, a.N = desc->N, a.K = desc->K;
+  a.lda = desc->a_rs, a.ldb = desc->b_cs, a.ldd = desc->d_rs;
+  a.a_bytes = a.M > 0 ? (a.M - 1) * a.lda + a.K : 0;
+  a.b_bytes = a.N > 0 ? (a.N - 1) * a.ldb + a.K : 0;
+  set_tiles(a);
+  p->variant = migemm::scaled_variant(a.M, a.N, a.K, cus);
+  p->grid = a.num_tiles < cus ? a.num_tiles : cus;
+  return add_live(p, kScaled, out);
+}
+
+int gemm_scaled_plan_destroy(migemm_scaled_plan* plan) { return destroy(plan, kScaled); }
+
+size_t gemm_scaled_workspace_size(const migemm_scaled_plan* plan) {
+  (void)plan;
+  return 0;
+}
+
+int gemm_scaled_run(const migemm_scaled_plan* p, const void* a, const float* a_scale, const void* b,
+                    const float* b_scale, void* d, void* workspace, void* stream) {
+  (void)workspace;
+  if (!is_live(p, kScaled)) return MIGEMM_ERR_INVALID_ARG;
+  const migemm_scaled_desc& e = p->desc;
+  if (e.M == 0 || e.N == 0) return MIGEMM_OK;
+  if (!a_scale || !b_scale || !d || (e.K > 0 && (!a || !b))) return MIGEMM_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(d, 16) || !aligned(a_scale, 16) ||
+      !aligned(b_scale, 16))
+    return MIGEMM_ERR_MISALIGNED;
+  if (!current_device_is(e.device)) return MIGEMM_ERR_DEVICE;
+  migemm::ScaledArgs s = p->base;
+  s.gemm.A = a, s.gemm.B = b, s.gemm.D = d;
+  s.a_scale = a_scale, s.b_scale = b_scale;
+  return launched(migemm::launch_scaled(s, p->variant, p->grid, static_cast<hipStream_t>(stream)));
+}
+
+int gemm_norm_desc_validate(const migemm_norm_desc* desc) { return validate_norm(desc); }
+
+int gemm_norm_plan_create(const migemm_norm_desc* desc, migemm_norm_plan** out) {
+  if (!out) return MIGEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  int st = validate_norm(desc);
+  if (st != MIGEMM_OK) return st;
+  int cus = 0;
+  st = check_device(desc->device, &cus);
+  if (st != MIGEMM_OK) return st;
+  migemm_norm_plan* p = new (std::nothrow) migemm_norm_plan();
+  if (!p) return MIGEMM_ERR_INVALID_ARG;
+  p->desc = *desc;
+  if (norm_backward(*desc)) {
+    p->partial_rows = migemm::norm_partial_rows(desc->rows, desc->cols, cus);
+    p->workspace_bytes = (size_t)(p->partial_rows * desc->cols * 4);
+  }
+  return add_live(p, kNorm, out);
+}
+
+int gemm_norm_plan_destroy(migemm_norm_plan* plan) { return destroy(plan, kNorm); }
+
+size_t gemm_norm_workspace_size(const migemm_norm_plan* plan) {
+  return is_live(plan, kNorm) ? plan->workspace_bytes : 0;
+}
+
+int gemm_norm_run(const migemm_norm_plan* p, const void* x, const void* r, const void* weight,
+                  void* h, void* y, float* scale, float* rstd, void* stream) {
+  if (!is_live(p, kNorm)) return MIGEMM_ERR_INVALID_ARG;
+  const migemm_norm_desc& d = p->desc;
+  if (d.rows == 0) return MIGEMM_OK;
+  const bool res = norm_residual(d), e4m3 = d.y_type == MIGEMM_FP8_E4M3;
+  if ((r != nullptr) != res || (h != nullptr) != res || (scale != nullptr) != e4m3)
+    return MIGEMM_ERR_INVALID_ARG;
+  if (!x || !weight || !y || !rstd) return MIGEMM_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(r, 16) || !aligned(weight, 16) || !aligned(h, 16) ||
+      !aligned(y, 16) || !aligned(scale, 4) || !aligned(rstd, 4))
+    return MIGEMM_ERR_MISALIGNED;
+  if (!current_device_is(d.device)) return MIGEMM_ERR_DEVICE;
+  migemm::NormArgs a = {};
+  a.x = x, a.r = r, a.weight = weight, a.h = h, a.y = y, a.scale = scale, a.rstd = rstd;
+  a.rows = d.rows, a.cols = d.cols, a.eps = d.eps;
+  a.x_rs = d.x_rs, a.r_rs = d.r_rs, a.h_rs = d.h_rs, a.y_rs = d.y_rs;
+  return launched(migemm::launch_norm_forward(a, e4m3, static_cast<hipStream_t>(stream)));
+}
+
+int gemm_norm_run_backward(const migemm_norm_plan* p, const void* dy, const void* h,
+                           const void* weight, const float* rstd, const void* dh, void* dx,
+                           float* dweight, void* workspace, void* stream) {
+  if (!is_live(p, kNorm) || !norm_backward(p->desc)) return MIGEMM_ERR_INVALID_ARG;
+  const migemm_norm_desc& d = p->desc;
+  if (!dweight) return MIGEMM_ERR_INVALID_ARG;
+  if (d.rows > 0 && (!dy || !h || !weight || !rstd || !dx || (dh != nullptr) != (d.dh_rs != 0)))
+    return MIGEMM_ERR_INVALID_ARG;
+  if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) ||
+      !aligned(dh, 16) || !aligned(dx, 16) || !aligned(dweight, 4))
+    return MIGEMM_ERR_MISALIGNED;
+  const int st = check_workspace(p->workspace_bytes, workspace);
+  if (st != MIGEMM_OK) return st;
+  if (!current_device_is(d.device)) return MIGEMM_ERR_DEVICE;
+  migemm::NormArgs a = {};
+  a.x = h, a.dy = dy, a.dh = dh, a.weight = weight, a.dx = dx, a.dweight = dweight;
+  a.rstd = const_cast<float*>(rstd), a.partials = static_cast<float*>(workspace);
+  a.rows = d.rows, a.cols = d.cols, a.partial_rows = p->partial_rows;
+  a.x_rs = norm_residual(d) ? d.h_rs : d.x_rs;
+  a.dy_rs = d.dy_rs, a.dh_rs = d.dh_rs, a.dx_rs = d.dx_rs;
+  return launched(migemm::launch_norm_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -42,6 +42,10 @@ EXPORTED = [
     "gemm_desc_validate", "gemm_plan_create", "gemm_plan_destroy", "gemm_plan_get_info",
     "gemm_plan_workspace_size", "gemm_workspace_init", "gemm_run", "gemm_run_with_tile_consumer",
     "gemm_run_no_alloc", "gemm_debug_read", "gemm_status_string",
+    "gemm_norm_desc_validate", "gemm_norm_plan_create", "gemm_norm_plan_destroy",
+    "gemm_norm_workspace_size", "gemm_norm_run", "gemm_norm_run_backward",
+    "gemm_scaled_desc_validate", "gemm_scaled_plan_create", "gemm_scaled_plan_destroy",
+    "gemm_scaled_workspace_size", "gemm_scaled_run",
 ]
 
 
@@ -83,6 +87,25 @@ class migemm_plan_info(ctypes.Structure):
         ("cu_count", ctypes.c_int32), ("handoff_slots", ctypes.c_int32),
         ("stream_k_tiles", ctypes.c_int64), ("stream_k_units_per_tile", ctypes.c_int32),
         ("c_in_k_loop", ctypes.c_int32), ("batches", ctypes.c_int64),
+    ]
+
+
+class migemm_norm_desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("x_rs", ctypes.c_int64), ("y_rs", ctypes.c_int64),
+        ("r_rs", ctypes.c_int64), ("h_rs", ctypes.c_int64),
+        ("dy_rs", ctypes.c_int64), ("dx_rs", ctypes.c_int64), ("dh_rs", ctypes.c_int64),
+        ("eps", ctypes.c_float), ("y_type", ctypes.c_int32),
+        ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class migemm_scaled_desc(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("a_rs", ctypes.c_int64), ("b_cs", ctypes.c_int64), ("d_rs", ctypes.c_int64),
+        ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -138,10 +161,29 @@ def load(path: str | None = None):
     lib.gemm_run_no_alloc.restype = i32
     lib.gemm_debug_read.argtypes = [vp, vp, vp, P(migemm_debug_info)]
     lib.gemm_debug_read.restype = i32
+    _declare_plan_calls(lib, "norm", migemm_norm_desc)
+    lib.gemm_norm_run.argtypes = [vp] * 9
+    lib.gemm_norm_run.restype = i32
+    lib.gemm_norm_run_backward.argtypes = [vp] * 10
+    lib.gemm_norm_run_backward.restype = i32
+    _declare_plan_calls(lib, "scaled", migemm_scaled_desc)
+    lib.gemm_scaled_run.argtypes = [vp] * 8
+    lib.gemm_scaled_run.restype = i32
     lib.gemm_status_string.argtypes = [i32]
     lib.gemm_status_string.restype = ctypes.c_char_p
     _lib = lib
     return lib
+
+
+def _declare_plan_calls(lib, kind, desc):
+    """The calls every operator's plan has."""
+    vp, i32, P = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER
+    for name, args, res in (("desc_validate", [P(desc)], i32),
+                            ("plan_create", [P(desc), P(vp)], i32),
+                            ("plan_destroy", [vp], i32),
+                            ("workspace_size", [vp], ctypes.c_size_t)):
+        f = getattr(lib, f"gemm_{kind}_{name}")
+        f.argtypes, f.restype = args, res
 
 
 def _ptr(x) -> int | None:
@@ -282,3 +324,97 @@ class Plan:
             except Exception:
                 pass
             self.handle = None
+
+
+def gemm_norm_desc_validate(desc: migemm_norm_desc) -> int:
+    return int(load().gemm_norm_desc_validate(ctypes.byref(desc)))
+
+
+def gemm_norm_run(plan, x, r, weight, h, y, scale, rstd, stream=None, check: bool = True) -> int:
+    st = load().gemm_norm_run(_plan(plan), _ptr(x), _ptr(r), _ptr(weight), _ptr(h), _ptr(y),
+                              _ptr(scale), _ptr(rstd), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_norm_run")
+    return int(st)
+
+
+def gemm_norm_run_backward(plan, dy, h, weight, rstd, dh, dx, dweight, workspace=None, stream=None,
+                           check: bool = True) -> int:
+    st = load().gemm_norm_run_backward(_plan(plan), _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd),
+                                       _ptr(dh), _ptr(dx), _ptr(dweight), _ptr(workspace),
+                                       _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_norm_run_backward")
+    return int(st)
+
+
+def gemm_scaled_desc_validate(desc: migemm_scaled_desc) -> int:
+    return int(load().gemm_scaled_desc_validate(ctypes.byref(desc)))
+
+
+def gemm_scaled_run(plan, a, a_scale, b, b_scale, d, workspace=None, stream=None,
+                    check: bool = True) -> int:
+    st = load().gemm_scaled_run(_plan(plan), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(d),
+                                _ptr(workspace), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_scaled_run")
+    return int(st)
+
+
+class _OperatorPlan:
+    """Owns an operator's plan handle; destroys it when garbage-collected."""
+
+    kind = ""
+
+    def __init__(self, desc):
+        self.desc = desc
+        h = ctypes.c_void_p()
+        st = getattr(load(), f"gemm_{self.kind}_plan_create")(ctypes.byref(desc), ctypes.byref(h))
+        if st != MIGEMM_OK:
+            raise MigemmError(st, f"gemm_{self.kind}_plan_create")
+        self.handle = h.value
+
+    @property
+    def workspace_size(self) -> int:
+        return int(getattr(load(), f"gemm_{self.kind}_workspace_size")(self.handle))
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h:
+            try:
+                getattr(load(), f"gemm_{self.kind}_plan_destroy")(h)
+            except Exception:
+                pass
+            self.handle = None
+
+
+class NormPlan(_OperatorPlan):
+    """Residual addition and root-mean-square norm of rows x cols, y in bf16
+    or e4m3; row strides in elements.  r_rs and h_rs: with a residual; dy_rs
+    and dx_rs (and dh_rs): with a backward pass."""
+
+    kind = "norm"
+
+    def __init__(self, rows, cols, eps, y_type=MIGEMM_BF16, *, x_rs, y_rs, r_rs=0, h_rs=0, dy_rs=0,
+                 dx_rs=0, dh_rs=0, device=0):
+        super().__init__(migemm_norm_desc(rows, cols, x_rs, y_rs, r_rs, h_rs, dy_rs, dx_rs, dh_rs,
+                                          eps, y_type, device, 0))
+
+    def run(self, x, r, weight, h, y, scale, rstd, stream=None):
+        return gemm_norm_run(self, x, r, weight, h, y, scale, rstd, stream)
+
+    def run_backward(self, dy, h, weight, rstd, dh, dx, dweight, workspace=None, stream=None):
+        return gemm_norm_run_backward(self, dy, h, weight, rstd, dh, dx, dweight, workspace, stream)
+
+
+class ScaledPlan(_OperatorPlan):
+    """d (M x N bf16) = a (M x K e4m3, a scale per row) times the transpose of
+    b (N x K e4m3, a scale per row); row strides in elements."""
+
+    kind = "scaled"
+
+    def __init__(self, M, N, K, *, a_rs, b_cs, d_rs, device=0):
+        super().__init__(migemm_scaled_desc(M, N, K, a_rs, b_cs, d_rs, device, 0))
+
+    def run(self, a, a_scale, b, b_scale, d, workspace=None, stream=None):
+        return gemm_scaled_run(self, a, a_scale, b, b_scale, d, workspace, stream)
