@@ -454,6 +454,49 @@ size_t gemm_scaled_workspace_size(const migemm_scaled_plan* plan);
 int gemm_scaled_run(const migemm_scaled_plan* plan, const void* a, const float* a_scale,
                     const void* b, const float* b_scale, void* d, void* workspace, void* stream);
 
+/* Softmax cross entropy over a vocabulary, from the hidden states x (rows x
+ * hidden) and the output projection's weights w (vocab x hidden), both bf16,
+ * without the logits in memory:
+ *   logits = x w^T (fp32);   lse = log of the sum of exp(logits) of a row
+ *   loss = lse - logits[target], 0 where target < 0 (a row that does not
+ *   count: a prompt's token, padding), NaN where target >= vocab
+ * and with g = (exp(logits - lse) - onehot(target)) * dloss
+ *   dx = bf16(g w),   dw = bf16(g^T x)
+ * where a row whose target is not in [0, vocab) has g = 0 exactly, whatever
+ * x and dloss hold there: its dx is 0, and it adds nothing to dw.  lse is
+ * written for every row.  g is rounded to bf16 on its way into the two
+ * products, whose sums are fp32.  rows may be 0, vocab and hidden are at
+ * least 1; rows and vocab below 2^28, and 256 rows of each matrix span less
+ * than 2^31 bytes (else UNSUPPORTED). */
+typedef struct migemm_vocab_loss_desc {
+  int64_t rows, vocab, hidden;
+  int64_t x_rs, w_rs;
+  int64_t dx_rs, dw_rs; /* backward pass; both 0: none */
+  int32_t device;
+  int32_t reserved; /* must be 0 */
+} migemm_vocab_loss_desc;
+
+typedef struct migemm_vocab_loss_plan migemm_vocab_loss_plan; /* opaque, host memory only */
+
+int gemm_vocab_loss_desc_validate(const migemm_vocab_loss_desc* desc);
+int gemm_vocab_loss_plan_create(const migemm_vocab_loss_desc* desc, migemm_vocab_loss_plan** out);
+int gemm_vocab_loss_plan_destroy(migemm_vocab_loss_plan* plan);
+/* Bytes of workspace either run needs (256-byte aligned).  Forward: 8 bytes a
+ * row (of up to 16384) and 128 vocabulary entries.  Backward: the rows that
+ * count, one piece of g (up to 512 MiB) and fp32 sums of dx. */
+size_t gemm_vocab_loss_workspace_size(const migemm_vocab_loss_plan* plan);
+
+/* target is int64 [rows]; loss and lse are fp32 [rows]. */
+int gemm_vocab_loss_run(const migemm_vocab_loss_plan* plan, const void* x, const void* w,
+                        const int64_t* target, float* loss, float* lse, void* workspace,
+                        void* stream);
+
+/* lse is what the forward run wrote, dloss fp32 [rows] the gradient of each
+ * row's loss.  dx and dw are written whole. */
+int gemm_vocab_loss_run_backward(const migemm_vocab_loss_plan* plan, const void* x, const void* w,
+                                 const int64_t* target, const float* lse, const float* dloss,
+                                 void* dx, void* dw, void* workspace, void* stream);
+
 /* Static text for a status code (never NULL).  No counterpart on the pages. */
 const char* gemm_status_string(int status);
 

@@ -22,7 +22,7 @@ SOURCES = [os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "gemm_kernels.hip")
 # The operators around the product: their C ABI layer and kernel units.
 OPERATORS = os.path.join(CSRC, "operators")
 OPERATOR_API = os.path.join(OPERATORS, "operators_api.cpp")
-OPERATOR_KERNELS = ["norm_kernels", "scaled_kernels"]
+OPERATOR_KERNELS = ["norm_kernels", "scaled_kernels", "loss_kernels"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

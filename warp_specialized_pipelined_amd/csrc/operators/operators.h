@@ -60,4 +60,48 @@ int scaled_variant(int64_t M, int64_t N, int64_t K, int cu_count);
 hipError_t prepare_scaled();
 hipError_t launch_scaled(const ScaledArgs& a, int variant, int grid, hipStream_t stream);
 
+// ------------------------------------------------------------------- loss
+
+// Four fp32 sums of dx.
+typedef float dx_piece __attribute__((ext_vector_type(4)));
+
+struct LossArgs {
+  KernelArgs gemm;        // the product a kernel forms
+  int64_t T, V, H;
+  const void* x;          // the caller's, T x H
+  int64_t x_rs, dx_rs;
+  const int64_t* target;
+  // Forward.  (target, loss, lse and target_logit start at the first of the
+  // gemm.M rows that a launch takes.)
+  float* loss;
+  float* lse;             // backward: in
+  float2* parts;          // [V / 128][part_rows]: largest logit, sum of exponentials
+  int64_t part_rows;
+  float* target_logit;
+  // Backward.
+  const float* dloss;
+  void* dx;
+  int* count;             // rows that count
+  int* place;             // [T]
+  int* from;              // [count]
+  unsigned short* rows_x; // [count][rows_ld]
+  int64_t rows_ld;
+  float* rows_lse;
+  float* rows_dloss;
+  int* rows_target;
+  int64_t first_col;      // the piece's first vocabulary entry
+  dx_piece* dx_sums;    // [splits][dx_tiles] tiles of fp32 sums in register order
+  int64_t dx_tiles;
+  int32_t splits;
+  int32_t first_piece;
+};
+
+hipError_t prepare_loss();
+hipError_t launch_loss_forward(const LossArgs& s, int grid, hipStream_t stream);
+hipError_t launch_loss_rows(const LossArgs& s, hipStream_t stream);
+hipError_t launch_loss_gradient(const LossArgs& s, int grid, hipStream_t stream);
+hipError_t launch_loss_dw(const LossArgs& s, int grid, hipStream_t stream);
+hipError_t launch_loss_dx(const LossArgs& s, int grid, hipStream_t stream);
+hipError_t launch_loss_dx_finish(const LossArgs& s, hipStream_t stream);
+
 }  // namespace migemm

@@ -17,6 +17,19 @@ struct migemm_scaled_plan {
   int variant, grid;
 };
 
+struct migemm_vocab_loss_plan {
+  migemm_vocab_loss_desc desc;
+  int cus;
+  // Forward: rows a launch takes (the workspace holds one launch's pairs).
+  int64_t chunk;
+  // Backward: vocabulary entries a piece, g's row stride, the ways K of dx is
+  // split, and where things lie in the workspace.
+  int64_t piece, g_rs, rows_rs, dx_tiles;
+  int splits;
+  size_t at_place, at_from, at_lse, at_dloss, at_target, at_rows, at_g, at_sums;
+  size_t workspace_bytes;
+};
+
 struct migemm_norm_plan {
   migemm_norm_desc desc;
   int64_t partial_rows;
@@ -169,9 +182,197 @@ int validate_scaled(const migemm_scaled_desc* d) {
   return MIGEMM_OK;
 }
 
+// --------------------------------------------------------------------- loss
+
+int validate_loss(const migemm_vocab_loss_desc* d) {
+  if (!d || d->rows < 0 || d->vocab < 1 || d->hidden < 1 || d->reserved != 0)
+    return MIGEMM_ERR_INVALID_ARG;
+  if ((d->dx_rs != 0) != (d->dw_rs != 0)) return MIGEMM_ERR_INVALID_ARG;
+  const bool back = d->dx_rs != 0;
+  int st = check_matrix(d->rows, d->hidden, d->x_rs, 2);
+  if (st == MIGEMM_OK) st = check_matrix(d->vocab, d->hidden, d->w_rs, 2);
+  if (st == MIGEMM_OK && back) st = check_matrix(d->rows, d->hidden, d->dx_rs, 2);
+  if (st == MIGEMM_OK && back) st = check_matrix(d->vocab, d->hidden, d->dw_rs, 2);
+  if (st != MIGEMM_OK) return st;
+  if (!band_fits(d->x_rs, 2) || !band_fits(d->w_rs, 2) ||
+      (back && (!band_fits(d->dx_rs, 2) || !band_fits(d->dw_rs, 2))))
+    return MIGEMM_ERR_UNSUPPORTED;
+  // Row numbers and vocabulary entries are 32-bit in the kernels.
+  if (d->rows >= ((int64_t)1 << 28) || d->vocab >= ((int64_t)1 << 28)) return MIGEMM_ERR_UNSUPPORTED;
+  if (!tiles_fit(d->rows, 16 * 256) || !tiles_fit(d->vocab, 16384)) return MIGEMM_ERR_UNSUPPORTED;
+  return MIGEMM_OK;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Rows of the forward pass a launch takes: their pairs of the whole
+// vocabulary are the workspace (at 131072 entries 128 MiB).
+constexpr int64_t kLossChunk = 16384;
+// The most a piece of g takes.
+constexpr int64_t kPieceBytes = (int64_t)512 << 20;
+
+void lay_out_loss(migemm_vocab_loss_plan* p) {
+  const migemm_vocab_loss_desc& d = p->desc;
+  const int64_t T = d.rows, V = d.vocab, H = d.hidden;
+  p->chunk = T < kLossChunk ? T : kLossChunk;
+  const int64_t parts = (V + migemm::kWaveTile - 1) / migemm::kWaveTile;
+  p->workspace_bytes = (size_t)(parts * p->chunk * 8 + p->chunk * 4);
+  if (d.dx_rs == 0) return;
+  // Pieces of g within kPieceBytes, of equal width.
+  int64_t most = kPieceBytes / 2 / up(T > 0 ? T : 1, 256) / 256 * 256;
+  most = most < 1024 ? 1024 : (most > (1 << 20) ? 1 << 20 : most);
+  const int64_t pieces = (V + most - 1) / most;
+  p->piece = up((V + pieces - 1) / pieces, 256);
+  p->g_rs = up(p->piece < V ? p->piece : V, 64) + 64;  // rows not a power of two apart
+  p->rows_rs = up(H, 64);
+  const int64_t tiles_m = (T + 255) / 256, tiles_n = (H + 255) / 256;
+  p->dx_tiles = tiles_m * tiles_n;
+  const int64_t stages = ((p->piece < V ? p->piece : V) + 63) / 64;
+  int64_t splits = p->dx_tiles > 0 ? p->cus / p->dx_tiles : 1;
+  splits = splits > stages ? stages : splits;
+  p->splits = (int)(splits < 1 ? 1 : splits);
+  size_t at = 256;  // the count
+  auto take = [&](int64_t bytes) {
+    const size_t from = at;
+    at += (size_t)up(bytes, 256);
+    return from;
+  };
+  p->at_place = take(T * 4);
+  p->at_from = take(T * 4);
+  p->at_lse = take(T * 4);
+  p->at_dloss = take(T * 4);
+  p->at_target = take(T * 4);
+  p->at_rows = take(T * p->rows_rs * 2);
+  p->at_g = take(T * p->g_rs * 2);
+  p->at_sums = take(p->splits * p->dx_tiles * migemm::kTileM * migemm::kTileN * 4);
+  if (at > p->workspace_bytes) p->workspace_bytes = at;
+}
+
+// M x N x K of bf16 operands with the given strides, in 256 x 256 tiles.
+migemm::KernelArgs product(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, bool a_kmajor,
+                           const void* B, int64_t ldb, bool b_kmajor, void* D, int64_t ldd) {
+  migemm::KernelArgs a = {};
+  a.M = M, a.N = N, a.K = K, a.A = A, a.B = B, a.D = D, a.lda = lda, a.ldb = ldb, a.ldd = ldd;
+  a.a_bytes = a_kmajor ? (M > 0 ? ((M - 1) * lda + K) * 2 : 0) : (K > 0 ? ((K - 1) * lda + M) * 2 : 0);
+  a.b_bytes = b_kmajor ? (N > 0 ? ((N - 1) * ldb + K) * 2 : 0) : (K > 0 ? ((K - 1) * ldb + N) * 2 : 0);
+  set_tiles(a);
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
+
+int gemm_vocab_loss_desc_validate(const migemm_vocab_loss_desc* desc) { return validate_loss(desc); }
+
+int gemm_vocab_loss_plan_create(const migemm_vocab_loss_desc* desc, migemm_vocab_loss_plan** out) {
+  if (!out) return MIGEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  int st = validate_loss(desc);
+  if (st != MIGEMM_OK) return st;
+  int cus = 0;
+  st = check_device(desc->device, &cus);
+  if (st != MIGEMM_OK) return st;
+  if (migemm::prepare_loss() != hipSuccess) return MIGEMM_ERR_DEVICE;
+  migemm_vocab_loss_plan* p = new (std::nothrow) migemm_vocab_loss_plan();
+  if (!p) return MIGEMM_ERR_INVALID_ARG;
+  p->desc = *desc;
+  p->cus = cus;
+  lay_out_loss(p);
+  return add_live(p, kVocabLoss, out);
+}
+
+int gemm_vocab_loss_plan_destroy(migemm_vocab_loss_plan* plan) { return destroy(plan, kVocabLoss); }
+
+size_t gemm_vocab_loss_workspace_size(const migemm_vocab_loss_plan* plan) {
+  return is_live(plan, kVocabLoss) ? plan->workspace_bytes : 0;
+}
+
+int gemm_vocab_loss_run(const migemm_vocab_loss_plan* p, const void* x, const void* w,
+                        const int64_t* target, float* loss, float* lse, void* workspace,
+                        void* stream) {
+  if (!is_live(p, kVocabLoss)) return MIGEMM_ERR_INVALID_ARG;
+  const migemm_vocab_loss_desc& d = p->desc;
+  if (d.rows == 0) return MIGEMM_OK;
+  if (!x || !w || !target || !loss || !lse) return MIGEMM_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4))
+    return MIGEMM_ERR_MISALIGNED;
+  const int st = check_workspace(p->workspace_bytes, workspace);
+  if (st != MIGEMM_OK) return st;
+  if (!current_device_is(d.device)) return MIGEMM_ERR_DEVICE;
+  migemm::LossArgs s = {};
+  s.V = d.vocab, s.H = d.hidden;
+  s.parts = static_cast<float2*>(workspace);
+  s.part_rows = p->chunk;
+  s.target_logit = reinterpret_cast<float*>(
+      s.parts + (d.vocab + migemm::kWaveTile - 1) / migemm::kWaveTile * p->chunk);
+  for (int64_t r = 0; r < d.rows; r += p->chunk) {
+    const int64_t rows = d.rows - r < p->chunk ? d.rows - r : p->chunk;
+    s.gemm = product(rows, d.vocab, d.hidden, static_cast<const char*>(x) + r * d.x_rs * 2, d.x_rs,
+                     true, w, d.w_rs, true, nullptr, 0);
+    s.target = target + r, s.loss = loss + r, s.lse = lse + r;
+    const int grid = s.gemm.num_tiles < p->cus ? s.gemm.num_tiles : p->cus;
+    const hipError_t e = migemm::launch_loss_forward(s, grid, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return MIGEMM_ERR_LAUNCH;
+  }
+  return MIGEMM_OK;
+}
+
+int gemm_vocab_loss_run_backward(const migemm_vocab_loss_plan* p, const void* x, const void* w,
+                                 const int64_t* target, const float* lse, const float* dloss, void* dx,
+                                 void* dw, void* workspace, void* stream) {
+  if (!is_live(p, kVocabLoss) || p->desc.dx_rs == 0) return MIGEMM_ERR_INVALID_ARG;
+  const migemm_vocab_loss_desc& d = p->desc;
+  if (!w || !dw || (d.rows > 0 && (!x || !target || !lse || !dloss || !dx)))
+    return MIGEMM_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(target, 8) || !aligned(lse, 4) ||
+      !aligned(dloss, 4) || !aligned(dx, 16) || !aligned(dw, 16))
+    return MIGEMM_ERR_MISALIGNED;
+  const int st = check_workspace(p->workspace_bytes, workspace);
+  if (st != MIGEMM_OK) return st;
+  if (!current_device_is(d.device)) return MIGEMM_ERR_DEVICE;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  migemm::LossArgs s = {};
+  s.T = d.rows, s.V = d.vocab, s.H = d.hidden;
+  s.x = x, s.x_rs = d.x_rs, s.dx = dx, s.dx_rs = d.dx_rs;
+  s.target = target, s.lse = const_cast<float*>(lse), s.dloss = dloss;
+  s.count = reinterpret_cast<int*>(ws);
+  s.place = reinterpret_cast<int*>(ws + p->at_place);
+  s.from = reinterpret_cast<int*>(ws + p->at_from);
+  s.rows_lse = reinterpret_cast<float*>(ws + p->at_lse);
+  s.rows_dloss = reinterpret_cast<float*>(ws + p->at_dloss);
+  s.rows_target = reinterpret_cast<int*>(ws + p->at_target);
+  s.rows_x = reinterpret_cast<unsigned short*>(ws + p->at_rows);
+  s.rows_ld = p->rows_rs;
+  s.dx_sums = reinterpret_cast<migemm::dx_piece*>(ws + p->at_sums);
+  s.dx_tiles = p->dx_tiles;
+  s.splits = p->splits;
+  void* g = ws + p->at_g;
+  if (migemm::launch_loss_rows(s, hs) != hipSuccess) return MIGEMM_ERR_LAUNCH;
+  auto grid = [&](int64_t items) { return (int)(items < p->cus ? items : p->cus); };
+  for (int64_t c = 0; c < d.vocab; c += p->piece) {
+    const int64_t cols = d.vocab - c < p->piece ? d.vocab - c : p->piece;
+    const char* wc = static_cast<const char*>(w) + c * d.w_rs * 2;
+    s.first_col = c;
+    s.first_piece = c == 0;
+    if (d.rows > 0) {
+      s.gemm = product(d.rows, cols, d.hidden, s.rows_x, s.rows_ld, true, wc, d.w_rs, true, g, p->g_rs);
+      if (migemm::launch_loss_gradient(s, grid(s.gemm.num_tiles), hs) != hipSuccess)
+        return MIGEMM_ERR_LAUNCH;
+    }
+    s.gemm = product(cols, d.hidden, d.rows, g, p->g_rs, false, s.rows_x, s.rows_ld, false,
+                     static_cast<char*>(dw) + c * d.dw_rs * 2, d.dw_rs);
+    if (migemm::launch_loss_dw(s, grid(s.gemm.num_tiles), hs) != hipSuccess) return MIGEMM_ERR_LAUNCH;
+    if (d.rows > 0) {
+      s.gemm = product(d.rows, d.hidden, cols, g, p->g_rs, true, wc, d.w_rs, false, nullptr, 0);
+      if (migemm::launch_loss_dx(s, grid(s.gemm.num_tiles * (int64_t)p->splits), hs) != hipSuccess)
+        return MIGEMM_ERR_LAUNCH;
+    }
+  }
+  if (d.rows > 0 && migemm::launch_loss_dx_finish(s, hs) != hipSuccess) return MIGEMM_ERR_LAUNCH;
+  return MIGEMM_OK;
+}
 
 int gemm_scaled_desc_validate(const migemm_scaled_desc* desc) { return validate_scaled(desc); }
 

@@ -46,6 +46,8 @@ EXPORTED = [
     "gemm_norm_workspace_size", "gemm_norm_run", "gemm_norm_run_backward",
     "gemm_scaled_desc_validate", "gemm_scaled_plan_create", "gemm_scaled_plan_destroy",
     "gemm_scaled_workspace_size", "gemm_scaled_run",
+    "gemm_vocab_loss_desc_validate", "gemm_vocab_loss_plan_create", "gemm_vocab_loss_plan_destroy",
+    "gemm_vocab_loss_workspace_size", "gemm_vocab_loss_run", "gemm_vocab_loss_run_backward",
 ]
 
 
@@ -105,6 +107,15 @@ class migemm_scaled_desc(ctypes.Structure):
     _fields_ = [
         ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
         ("a_rs", ctypes.c_int64), ("b_cs", ctypes.c_int64), ("d_rs", ctypes.c_int64),
+        ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class migemm_vocab_loss_desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("hidden", ctypes.c_int64),
+        ("x_rs", ctypes.c_int64), ("w_rs", ctypes.c_int64),
+        ("dx_rs", ctypes.c_int64), ("dw_rs", ctypes.c_int64),
         ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
@@ -169,6 +180,11 @@ def load(path: str | None = None):
     _declare_plan_calls(lib, "scaled", migemm_scaled_desc)
     lib.gemm_scaled_run.argtypes = [vp] * 8
     lib.gemm_scaled_run.restype = i32
+    _declare_plan_calls(lib, "vocab_loss", migemm_vocab_loss_desc)
+    lib.gemm_vocab_loss_run.argtypes = [vp] * 8
+    lib.gemm_vocab_loss_run.restype = i32
+    lib.gemm_vocab_loss_run_backward.argtypes = [vp] * 10
+    lib.gemm_vocab_loss_run_backward.restype = i32
     lib.gemm_status_string.argtypes = [i32]
     lib.gemm_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -361,6 +377,29 @@ def gemm_scaled_run(plan, a, a_scale, b, b_scale, d, workspace=None, stream=None
     return int(st)
 
 
+def gemm_vocab_loss_desc_validate(desc: migemm_vocab_loss_desc) -> int:
+    return int(load().gemm_vocab_loss_desc_validate(ctypes.byref(desc)))
+
+
+def gemm_vocab_loss_run(plan, x, w, target, loss, lse, workspace=None, stream=None,
+                        check: bool = True) -> int:
+    st = load().gemm_vocab_loss_run(_plan(plan), _ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse),
+                                    _ptr(workspace), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_vocab_loss_run")
+    return int(st)
+
+
+def gemm_vocab_loss_run_backward(plan, x, w, target, lse, dloss, dx, dw, workspace=None, stream=None,
+                                 check: bool = True) -> int:
+    st = load().gemm_vocab_loss_run_backward(_plan(plan), _ptr(x), _ptr(w), _ptr(target), _ptr(lse),
+                                             _ptr(dloss), _ptr(dx), _ptr(dw), _ptr(workspace),
+                                             _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_vocab_loss_run_backward")
+    return int(st)
+
+
 class _OperatorPlan:
     """Owns an operator's plan handle; destroys it when garbage-collected."""
 
@@ -418,3 +457,20 @@ class ScaledPlan(_OperatorPlan):
 
     def run(self, a, a_scale, b, b_scale, d, workspace=None, stream=None):
         return gemm_scaled_run(self, a, a_scale, b, b_scale, d, workspace, stream)
+
+
+class VocabLossPlan(_OperatorPlan):
+    """Softmax cross entropy of rows x hidden states over a vocabulary's
+    vocab x hidden weights; row strides in elements.  dx_rs and dw_rs: with
+    a backward pass."""
+
+    kind = "vocab_loss"
+
+    def __init__(self, rows, vocab, hidden, *, x_rs, w_rs, dx_rs=0, dw_rs=0, device=0):
+        super().__init__(migemm_vocab_loss_desc(rows, vocab, hidden, x_rs, w_rs, dx_rs, dw_rs, device, 0))
+
+    def run(self, x, w, target, loss, lse, workspace=None, stream=None):
+        return gemm_vocab_loss_run(self, x, w, target, loss, lse, workspace, stream)
+
+    def run_backward(self, x, w, target, lse, dloss, dx, dw, workspace=None, stream=None):
+        return gemm_vocab_loss_run_backward(self, x, w, target, lse, dloss, dx, dw, workspace, stream)
