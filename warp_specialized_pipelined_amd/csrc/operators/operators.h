@@ -48,17 +48,26 @@ hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream);
 
 // ----------------------------------------------------------------- scaled
 
+// Four fp32 sums.
+typedef float mid_piece __attribute__((ext_vector_type(4)));
+
 struct ScaledArgs {
   KernelArgs gemm;       // A, B: e4m3, K-contiguous; strides in elements
   const float* a_scale;  // [M]
   const float* b_scale;  // [N], 16-byte aligned
+  mid_piece* partials;   // workspace: the splits' sums
+  int32_t splits;
 };
 
-// Which kernel takes a product: 0 for 256 x 256 tiles, else a variant of the
-// small tiles.
-int scaled_variant(int64_t M, int64_t N, int64_t K, int cu_count);
+// Which kernel takes a product, into how many ranges K is split, and the
+// workspace that takes.
+struct ScaledChoice {
+  int variant, splits;
+  int64_t workspace_bytes;
+};
+ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count);
 hipError_t prepare_scaled();
-hipError_t launch_scaled(const ScaledArgs& a, int variant, int grid, hipStream_t stream);
+hipError_t launch_scaled(const ScaledArgs& a, int variant, int cu_count, hipStream_t stream);
 
 // ------------------------------------------------------------------- loss
 

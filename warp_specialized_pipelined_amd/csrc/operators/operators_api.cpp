@@ -14,7 +14,8 @@
 struct migemm_scaled_plan {
   migemm_scaled_desc desc;
   migemm::ScaledArgs base;  // the shape's part of the kernel arguments
-  int variant, grid;
+  int variant, cus;
+  size_t workspace_bytes;
 };
 
 struct migemm_vocab_loss_plan {
@@ -394,21 +395,22 @@ int gemm_scaled_plan_create(const migemm_scaled_desc* desc, migemm_scaled_plan**
   a.a_bytes = a.M > 0 ? (a.M - 1) * a.lda + a.K : 0;
   a.b_bytes = a.N > 0 ? (a.N - 1) * a.ldb + a.K : 0;
   set_tiles(a);
-  p->variant = migemm::scaled_variant(a.M, a.N, a.K, cus);
-  p->grid = a.num_tiles < cus ? a.num_tiles : cus;
+  const migemm::ScaledChoice c = migemm::choose_scaled(a.M, a.N, a.K, cus);
+  p->variant = c.variant;
+  p->base.splits = c.splits;
+  p->workspace_bytes = (size_t)c.workspace_bytes;
+  p->cus = cus;
   return add_live(p, kScaled, out);
 }
 
 int gemm_scaled_plan_destroy(migemm_scaled_plan* plan) { return destroy(plan, kScaled); }
 
 size_t gemm_scaled_workspace_size(const migemm_scaled_plan* plan) {
-  (void)plan;
-  return 0;
+  return is_live(plan, kScaled) ? plan->workspace_bytes : 0;
 }
 
 int gemm_scaled_run(const migemm_scaled_plan* p, const void* a, const float* a_scale, const void* b,
                     const float* b_scale, void* d, void* workspace, void* stream) {
-  (void)workspace;
   if (!is_live(p, kScaled)) return MIGEMM_ERR_INVALID_ARG;
   const migemm_scaled_desc& e = p->desc;
   if (e.M == 0 || e.N == 0) return MIGEMM_OK;
@@ -416,11 +418,14 @@ int gemm_scaled_run(const migemm_scaled_plan* p, const void* a, const float* a_s
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(d, 16) || !aligned(a_scale, 16) ||
       !aligned(b_scale, 16))
     return MIGEMM_ERR_MISALIGNED;
+  const int st = check_workspace(p->workspace_bytes, workspace);
+  if (st != MIGEMM_OK) return st;
   if (!current_device_is(e.device)) return MIGEMM_ERR_DEVICE;
   migemm::ScaledArgs s = p->base;
   s.gemm.A = a, s.gemm.B = b, s.gemm.D = d;
   s.a_scale = a_scale, s.b_scale = b_scale;
-  return launched(migemm::launch_scaled(s, p->variant, p->grid, static_cast<hipStream_t>(stream)));
+  s.partials = static_cast<migemm::mid_piece*>(workspace);
+  return launched(migemm::launch_scaled(s, p->variant, p->cus, static_cast<hipStream_t>(stream)));
 }
 
 int gemm_norm_desc_validate(const migemm_norm_desc* desc) { return validate_norm(desc); }

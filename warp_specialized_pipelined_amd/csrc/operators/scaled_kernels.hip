@@ -3,11 +3,14 @@
 //   d[m][n] = bf16(a_scale[m] b_scale[n] sum_k a[m][k] b[n][k])
 // a and b are e4m3 codes, K-contiguous; the sum is fp32.
 //
-// Two kernels.  scaled_tile: 256 x 256 tiles with the GEMM's K loop, where
-// the product is large enough to fill the chip with them (bound by the matrix
-// instructions).  scaled_rows: small tiles whose waves split K, for few rows
-// or columns (bound by reading the weights, or by latency).
+// scaled_tile: 256 x 256 tiles with the GEMM's K loop, where the product fills
+// the chip with them (bound by the matrix instructions).  scaled_mid: smaller
+// tiles, their K split where there are few (bound by loads into LDS).
+// scaled_rows: tiles of 16 to 64 rows whose waves split K (bound by reading
+// the weights, or by latency).
 #include <hip/hip_runtime.h>
+
+#include <math.h>
 
 #include <type_traits>
 
@@ -16,6 +19,7 @@
 #include "../kernel/mainloop.hpp"
 #include "../kernel/params.hpp"
 #include "../kernel/scheduler.hpp"
+#include "midtile.hpp"
 #include "operators.h"
 #include "rowblock.hpp"
 #include "tile_store.hpp"
@@ -85,60 +89,205 @@ __global__ __launch_bounds__(64 * W) void scaled_rows(ScaledArgs s) {
   rowblock_join<MB, NB, W>(acc, part, wave, lane, [&](int mb, int nb, f32x4 v) {
     const int64_t m = m0 + 16 * mb + (lane & 15), n = n0 + 16 * nb + 4 * (lane >> 4);
     if (m >= a.M || n >= a.N) return;
-    unsigned short* d = static_cast<unsigned short*>(a.D) + m * a.ldd + n;
     const float sa = s.a_scale[m];
-    float o[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = n + c < a.N ? v[c] * sa * s.b_scale[n + c] : 0.0f;
-    const u32x2 w = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-    if (n + 4 <= a.N) {
-      *reinterpret_cast<u32x2*>(d) = w;
-    } else {
-      for (int c = 0; c < (int)(a.N - n); ++c) d[c] = (unsigned short)(w[c >> 1] >> (16 * (c & 1)));
-    }
+    for (int c = 0; c < 4; ++c) v[c] = n + c < a.N ? v[c] * sa * s.b_scale[n + c] : 0.0f;
+    store4(static_cast<unsigned short*>(a.D) + m * a.ldd + n, a.N - n, v);
   });
 }
 
-// The variants of scaled_rows: 16-row blocks, 16-column blocks, waves.
-struct RowsVariant {
-  int mb, nb, waves;
+// Row scales and column scales of a wave's 32 BM x 32 BN part at (m0, n0).
+// Scales past the matrix read as zero; what they scale is not stored.
+template <int BM, int BN>
+struct Scales {
+  float rows[BM];
+  f32x4 cols[BN][4];
+  __device__ __forceinline__ void load(const ScaledArgs& s, int64_t m0, int64_t n0, int lane) {
+    auto vec = [](const float* p, int64_t from, int64_t n) {
+      int64_t left = (n - from) * 4;
+      left = left < 0 ? 0 : (left > 512 ? 512 : left);
+      return make_rsrc(p + from, (uint32_t)left);
+    };
+    const __amdgpu_buffer_rsrc_t ra = vec(s.a_scale, m0, s.gemm.M), rb = vec(s.b_scale, n0, s.gemm.N);
+#pragma unroll
+    for (int i = 0; i < BM; ++i)
+      rows[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, (32 * i + (lane & 31)) * 4, 0, 0));
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        cols[j][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   rb, (32 * j + 8 * q + 4 * (lane >> 5)) * 4, 0, 0));
+  }
+  __device__ __forceinline__ f32x4 apply(f32x4 v, int bi, int bj, int q) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = v[c] * rows[bi] * cols[bj][q][c];
+    return v;
+  }
+};
+
+// TM x TN tiles (midtile.hpp), a workgroup for each of a tile's `splits`
+// ranges of K stages.  With one it stores the result; with more each stores
+// its fp32 sums in register order, and scaled_join adds them up.
+template <bool EXACT, int TM, int TN, int SLOTS>
+__global__ __launch_bounds__(256, TM * TN <= 64 * 64 ? 4 : (TM * TN <= 64 * 128 ? 2 : 1)) void scaled_mid(ScaledArgs s) {
+  typedef MidGeom<TM, TN, SLOTS> G;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const KernelArgs& a = s.gemm;
+  const int tiles_m = (int)((a.M + TM - 1) / TM), tiles_n = (int)((a.N + TN - 1) / TN);
+  const int slot = persistent_slot(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
+  const int split = slot / tiles, tile = slot - split * tiles;
+  const MidTile t = mid_tile(tile, tiles_m, tiles_n);
+  const int stages = (int)((a.K + kStageKBytes - 1) / kStageKBytes);
+  const int k0 = (int)((int64_t)stages * split / s.splits), k1 = (int)((int64_t)stages * (split + 1) / s.splits);
+  const int64_t kend = (int64_t)k1 * kStageKBytes < a.K ? (int64_t)k1 * kStageKBytes : a.K;
+  MidAccum<G::kBM, G::kBN> acc;
+  mid_loop<1, true, true, TM, TN, SLOTS, EXACT>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0,
+                                                k1 - k0, kend);
+  const int64_t m0 = (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM;
+  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN;
+  if (s.splits > 1) {
+    mid_put(s.partials, slot, acc, wave, lane);
+    return;
+  }
+  Scales<G::kBM, G::kBN> scales;
+  scales.load(s, m0, n0, lane);
+  mid_store<G::kBM, G::kBN>(
+      a.D, a.ldd, a.M, a.N, m0, n0, wave, lane,
+      [&](int bi, int bj, int q) {
+        const f32x16& v = acc.v[bi][bj];
+        return scales.apply(f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}, bi, bj, q);
+      },
+      [](int64_t r) { return r; });
+}
+
+// The splits' sums of one 32 x 32 block, added in order, scaled and stored: a
+// wave a block.
+template <int TM, int TN>
+__global__ __launch_bounds__(64) void scaled_join(ScaledArgs s) {
+  constexpr int BM = TM / 64, BN = TN / 64;
+  const int lane = threadIdx.x;
+  const KernelArgs& a = s.gemm;
+  const int tiles_m = (int)((a.M + TM - 1) / TM), tiles_n = (int)((a.N + TN - 1) / TN);
+  const int part = blockIdx.x % (4 * BM * BN), tile = blockIdx.x / (4 * BM * BN);
+  const int wave = part / (BM * BN), block = part % (BM * BN);
+  const MidTile t = mid_tile(tile, tiles_m, tiles_n);
+  const int64_t m0 = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM + 32 * (block / BN);
+  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN + 32 * (block % BN);
+  if (m0 >= a.M || n0 >= a.N) return;
+  Scales<1, 1> scales;
+  scales.load(s, m0, n0, lane);
+  MidAccum<1, 1> acc = {};
+  for (int i = 0; i < s.splits; ++i) mid_add<BM, BN>(s.partials, i * tiles_m * tiles_n + tile, acc, wave, block, lane);
+  const int64_t m = m0 + (lane & 31);
+  if (m >= a.M) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t n = n0 + 8 * q + 4 * (lane >> 5);
+    const f32x16& v = acc.v[0][0];
+    const f32x4 x = scales.apply(f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}, 0, 0, q);
+    store4(static_cast<unsigned short*>(a.D) + m * a.ldd + n, a.N - n, x);
+  }
+}
+
+// The kernels a product can take: TM x TN tiles, one a workgroup (256 x 256:
+// one after another).  join: the tile's K may be split.
+struct Variant {
+  int tm, tn, threads, lds;
   void (*kernel)(ScaledArgs);
+  void (*join)(ScaledArgs);
+  // What its tiles cost (choose_scaled), in microseconds: a K stage of 128
+  // with one tile a compute unit and with two, and a tile besides.
+  double stage1, stage2, tile;
 };
-const RowsVariant kRows[] = {
-    {1, 1, 16, scaled_rows<1, 1, 1, 16, 2>},
-    {2, 2, 8, scaled_rows<1, 2, 2, 8, 1>},
-    {3, 2, 8, scaled_rows<1, 3, 2, 8, 1>},
-    {4, 2, 8, scaled_rows<1, 4, 2, 8, 1>},
-    {4, 4, 4, scaled_rows<1, 4, 4, 4, 1>},
-    {1, 4, 2, scaled_rows<kExactE4M3, 1, 4, 2, 1>},
-    {4, 4, 2, scaled_rows<kExactE4M3, 4, 4, 2, 1>},
+template <int ES, int MB, int NB, int W, int U>
+constexpr Variant rows_variant() {
+  return {16 * MB, 16 * NB, 64 * W, 0, scaled_rows<ES, MB, NB, W, U>, nullptr, 0, 0, 0};
+}
+template <bool EXACT, int TM, int TN, int SLOTS>
+constexpr Variant mid_variant(double stage1, double stage2, double tile) {
+  return {TM, TN, 256, (int)MidGeom<TM, TN, SLOTS>::kLds, scaled_mid<EXACT, TM, TN, SLOTS>,
+          EXACT ? nullptr : scaled_join<TM, TN>, stage1, stage2, tile};
+}
+enum { kTile256, kRowsFirst, kRowsLast = 4, kMidFirst, kMidLast = 7, kExactRows, kExactMid };
+const Variant kVariants[] = {
+    {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile, nullptr, 0.90, 0, 5.4},
+    rows_variant<1, 1, 1, 16, 2>(),
+    rows_variant<1, 1, 2, 16, 1>(),
+    rows_variant<1, 2, 2, 8, 1>(),
+    rows_variant<1, 4, 2, 8, 1>(),
+    mid_variant<false, 64, 64, 4>(0.32, 0.44, 1.7),
+    mid_variant<false, 64, 128, 3>(0.35, 0.54, 2.0),
+    mid_variant<false, 128, 128, 4>(0.37, 0, 4.3),
+    rows_variant<kExactE4M3, 1, 4, 2, 1>(),
+    mid_variant<true, 64, 64, 2>(0, 0, 0),
 };
+
+int64_t tiles_of(const Variant& v, int64_t M, int64_t N) {
+  return ((M + v.tm - 1) / v.tm) * ((N + v.tn - 1) / v.tn);
+}
+// Microseconds that v's kernel takes, after what the launch takes.
+double cost_of(const Variant& v, bool rows, int64_t M, int64_t N, int64_t K, int splits, int cu_count) {
+  const double tiles = (double)tiles_of(v, M, N), cus = cu_count;
+  if (rows) {
+    // Bound by what a compute unit takes in.
+    const double bytes = (double)((M < v.tm ? M : v.tm) + (N < v.tn ? N : v.tn)) * K;
+    return (tiles > cus ? tiles / cus : 1.0) * bytes / 47.8e3 + 0.5 * ceil(tiles / (2 * cus));
+  }
+  const double stages = ceil(ceil(K / 128.0) / splits), items = tiles * splits;
+  const double at_once = v.stage2 > 0 ? 2 * cus : cus;
+  const double full = floor(items / at_once), rest = items - full * at_once;
+  double t = full * (stages * (v.stage2 > 0 ? v.stage2 : v.stage1) + v.tile);
+  if (rest > 0) t += stages * (rest <= cus ? v.stage1 : v.stage2) + v.tile;
+  if (splits > 1) t += 3.3 + 2 * items * v.tm * v.tn * 4 / 4.0e6;  // scaled_join, and its sums to memory and back
+  return t;
+}
 
 }  // namespace
 
-int scaled_variant(int64_t M, int64_t N, int64_t K, int cu_count) {
+// The kernel that costs least: the figures are a fit to 260 products of 1 to
+// 8192 rows, 64 to 8192 columns and K of 257 to 16384, each timed with every
+// kernel and up to ten splits; what it picks is 2.3% slower than the fastest
+// of them on average.
+ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count) {
   // Short sums in exact products: with two K steps at most the time goes into
   // launch and output, whichever instruction multiplies.
-  if (K <= 256) return M <= 16 ? 6 : 7;
-  const int64_t tiles = ((M + kTileM - 1) / kTileM) * ((N + kTileN - 1) / kTileN);
-  if (M > 64 && tiles * 2 >= cu_count) return 0;
-  return M <= 16 ? 1 : (M <= 32 ? 2 : (M <= 48 ? 3 : (M <= 64 ? 4 : 5)));
+  if (K <= 256) return {M <= 16 ? kExactRows : kExactMid, 1, 0};
+  ScaledChoice best = {kTile256, 1, 0};
+  // (Every tile count fits 31 bits for the variants tried.)
+  double least = cost_of(kVariants[kTile256], false, M, N, K, 1, cu_count);
+  if ((double)M * N > 1e9) return best;
+  for (int i = kRowsFirst; i <= kMidLast; ++i)
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > 1 && (i <= kRowsLast || K < 128 * 3 * splits)) break;
+      const double cost = cost_of(kVariants[i], i <= kRowsLast, M, N, K, splits, cu_count);
+      if (cost >= least) continue;
+      least = cost;
+      best = {i, splits, 0};
+    }
+  const Variant& v = kVariants[best.variant];
+  if (best.splits > 1) best.workspace_bytes = tiles_of(v, M, N) * best.splits * v.tm * v.tn * 4;
+  return best;
 }
 
 hipError_t prepare_scaled() {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(scaled_tile),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, kPlainLdsBytes);
+  for (const Variant& v : kVariants) {
+    if (v.lds == 0) continue;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(v.kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, v.lds);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
-hipError_t launch_scaled(const ScaledArgs& s, int variant, int grid, hipStream_t stream) {
-  if (variant == 0) {
-    hipLaunchKernelGGL(scaled_tile, dim3(grid), dim3(kThreads), kPlainLdsBytes, stream, s);
-  } else {
-    const RowsVariant& v = kRows[variant - 1];
-    const int64_t tiles = ((s.gemm.M + 16 * v.mb - 1) / (16 * v.mb)) *
-                          ((s.gemm.N + 16 * v.nb - 1) / (16 * v.nb));
-    hipLaunchKernelGGL(v.kernel, dim3((uint32_t)tiles), dim3(64 * v.waves), 0, stream, s);
-  }
+hipError_t launch_scaled(const ScaledArgs& s, int variant, int cu_count, hipStream_t stream) {
+  const Variant& v = kVariants[variant];
+  const int64_t tiles = tiles_of(v, s.gemm.M, s.gemm.N);
+  const int64_t grid = variant == kTile256 ? (tiles < cu_count ? tiles : cu_count) : tiles * s.splits;
+  hipLaunchKernelGGL(v.kernel, dim3((uint32_t)grid), dim3(v.threads), v.lds, stream, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || s.splits == 1) return e;
+  hipLaunchKernelGGL(v.join, dim3((uint32_t)(tiles * (v.tm / 32) * (v.tn / 32))), dim3(64), 0, stream, s);
   return hipGetLastError();
 }
 
