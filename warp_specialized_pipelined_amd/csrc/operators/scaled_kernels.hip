@@ -211,14 +211,14 @@ constexpr Variant mid_variant(double stage1, double stage2, double tile) {
 }
 enum { kTile256, kRowsFirst, kRowsLast = 4, kMidFirst, kMidLast = 7, kExactRows, kExactMid };
 const Variant kVariants[] = {
-    {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile, nullptr, 0.90, 0, 5.4},
+    {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile, nullptr, 1.1, 0, 4.0},
     rows_variant<1, 1, 1, 16, 2>(),
     rows_variant<1, 1, 2, 16, 1>(),
     rows_variant<1, 2, 2, 8, 1>(),
     rows_variant<1, 4, 2, 8, 1>(),
-    mid_variant<false, 64, 64, 4>(0.32, 0.44, 1.7),
-    mid_variant<false, 64, 128, 3>(0.35, 0.54, 2.0),
-    mid_variant<false, 128, 128, 4>(0.37, 0, 4.3),
+    mid_variant<false, 64, 64, 4>(0.34, 0.53, 2.0),
+    mid_variant<false, 64, 128, 3>(0.38, 0.56, 1.9),
+    mid_variant<false, 128, 128, 4>(0.47, 0, 2.7),
     rows_variant<kExactE4M3, 1, 4, 2, 1>(),
     mid_variant<true, 64, 64, 2>(0, 0, 0),
 };
@@ -229,17 +229,20 @@ int64_t tiles_of(const Variant& v, int64_t M, int64_t N) {
 // Microseconds that v's kernel takes, after what the launch takes.
 double cost_of(const Variant& v, bool rows, int64_t M, int64_t N, int64_t K, int splits, int cu_count) {
   const double tiles = (double)tiles_of(v, M, N), cus = cu_count;
+  const double memory = ((double)M * K + (double)N * K + 2.0 * M * N) / 4.6e6;
   if (rows) {
     // Bound by what a compute unit takes in.
     const double bytes = (double)((M < v.tm ? M : v.tm) + (N < v.tn ? N : v.tn)) * K;
-    return (tiles > cus ? tiles / cus : 1.0) * bytes / 47.8e3 + 0.5 * ceil(tiles / (2 * cus));
+    const double t = (tiles > cus ? tiles / cus : 1.0) * bytes / 48e3;
+    return (t > memory ? t : memory) + 0.6 * ceil(tiles / (2 * cus));
   }
   const double stages = ceil(ceil(K / 128.0) / splits), items = tiles * splits;
   const double at_once = v.stage2 > 0 ? 2 * cus : cus;
   const double full = floor(items / at_once), rest = items - full * at_once;
   double t = full * (stages * (v.stage2 > 0 ? v.stage2 : v.stage1) + v.tile);
   if (rest > 0) t += stages * (rest <= cus ? v.stage1 : v.stage2) + v.tile;
-  if (splits > 1) t += 3.3 + 2 * items * v.tm * v.tn * 4 / 4.0e6;  // scaled_join, and its sums to memory and back
+  t = t > memory ? t : memory;
+  if (splits > 1) t += 3.9 + 2 * items * v.tm * v.tn * 4 / 5.0e6;  // scaled_join, and its sums to memory and back
   return t;
 }
 
@@ -247,7 +250,7 @@ double cost_of(const Variant& v, bool rows, int64_t M, int64_t N, int64_t K, int
 
 // The kernel that costs least: the figures are a fit to 260 products of 1 to
 // 8192 rows, 64 to 8192 columns and K of 257 to 16384, each timed with every
-// kernel and up to ten splits; what it picks is 2.3% slower than the fastest
+// kernel and up to ten splits; what it picks is 2.4% slower than the fastest
 // of them on average.
 ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count) {
   // Short sums in exact products: with two K steps at most the time goes into
