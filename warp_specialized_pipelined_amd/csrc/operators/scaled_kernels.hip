@@ -196,31 +196,32 @@ struct Variant {
   int tm, tn, threads, lds;
   void (*kernel)(ScaledArgs);
   void (*join)(ScaledArgs);
+  int per_cu;  // tiles a compute unit takes at once, for the cost
   // What its tiles cost (choose_scaled), in microseconds: a K stage of 128
   // with one tile a compute unit and with two, and a tile besides.
   double stage1, stage2, tile;
 };
 template <int ES, int MB, int NB, int W, int U>
-constexpr Variant rows_variant() {
-  return {16 * MB, 16 * NB, 64 * W, 0, scaled_rows<ES, MB, NB, W, U>, nullptr, 0, 0, 0};
+constexpr Variant rows_variant(int per_cu) {
+  return {16 * MB, 16 * NB, 64 * W, 0, scaled_rows<ES, MB, NB, W, U>, nullptr, per_cu, 0, 0, 0};
 }
 template <bool EXACT, int TM, int TN, int SLOTS>
-constexpr Variant mid_variant(double stage1, double stage2, double tile) {
+constexpr Variant mid_variant(int per_cu, double stage1, double stage2, double tile) {
   return {TM, TN, 256, (int)MidGeom<TM, TN, SLOTS>::kLds, scaled_mid<EXACT, TM, TN, SLOTS>,
-          EXACT ? nullptr : scaled_join<TM, TN>, stage1, stage2, tile};
+          EXACT ? nullptr : scaled_join<TM, TN>, per_cu, stage1, stage2, tile};
 }
 enum { kTile256, kRowsFirst, kRowsLast = 4, kMidFirst, kMidLast = 7, kExactRows, kExactMid };
 const Variant kVariants[] = {
-    {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile, nullptr, 1.1, 0, 4.0},
-    rows_variant<1, 1, 1, 16, 2>(),
-    rows_variant<1, 1, 2, 16, 1>(),
-    rows_variant<1, 2, 2, 8, 1>(),
-    rows_variant<1, 4, 2, 8, 1>(),
-    mid_variant<false, 64, 64, 4>(0.34, 0.53, 2.0),
-    mid_variant<false, 64, 128, 3>(0.38, 0.56, 1.9),
-    mid_variant<false, 128, 128, 4>(0.47, 0, 2.7),
-    rows_variant<kExactE4M3, 1, 4, 2, 1>(),
-    mid_variant<true, 64, 64, 2>(0, 0, 0),
+    {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile, nullptr, 1, 1.0, 1.0, 6.0},
+    rows_variant<1, 1, 1, 16, 2>(1),
+    rows_variant<1, 1, 2, 16, 1>(2),
+    rows_variant<1, 2, 2, 8, 1>(2),
+    rows_variant<1, 4, 2, 8, 1>(2),
+    mid_variant<false, 64, 64, 4>(2, 0.30, 0.48, 1.7),
+    mid_variant<false, 64, 128, 3>(2, 0.39, 0.62, 1.3),
+    mid_variant<false, 128, 128, 4>(1, 0.46, 0.46, 2.7),
+    rows_variant<kExactE4M3, 1, 4, 2, 1>(2),
+    mid_variant<true, 64, 64, 2>(2, 0, 0, 0),
 };
 
 int64_t tiles_of(const Variant& v, int64_t M, int64_t N) {
@@ -229,28 +230,27 @@ int64_t tiles_of(const Variant& v, int64_t M, int64_t N) {
 // Microseconds that v's kernel takes, after what the launch takes.
 double cost_of(const Variant& v, bool rows, int64_t M, int64_t N, int64_t K, int splits, int cu_count) {
   const double tiles = (double)tiles_of(v, M, N), cus = cu_count;
-  const double memory = ((double)M * K + (double)N * K + 2.0 * M * N) / 4.6e6;
+  const double memory = ((double)M * K + (double)N * K + 2.0 * M * N) / 5.5e6;
   if (rows) {
-    // Bound by what a compute unit takes in.
-    const double bytes = (double)((M < v.tm ? M : v.tm) + (N < v.tn ? N : v.tn)) * K;
-    const double t = (tiles > cus ? tiles / cus : 1.0) * bytes / 48e3;
-    return (t > memory ? t : memory) + 0.6 * ceil(tiles / (2 * cus));
+    // What a compute unit takes in, and the memory; they overlap in part.
+    const double rounds = tiles <= cus ? 1.0 : (v.per_cu == 1 ? ceil(tiles / cus) : tiles / cus);
+    const double cu = rounds * (v.tm + v.tn) * K / 52e3;
+    return (cu > memory ? cu + 0.26 * memory : memory + 0.26 * cu) + 0.6 * ceil(tiles / (2 * cus));
   }
   const double stages = ceil(ceil(K / 128.0) / splits), items = tiles * splits;
-  const double at_once = v.stage2 > 0 ? 2 * cus : cus;
-  const double full = floor(items / at_once), rest = items - full * at_once;
-  double t = full * (stages * (v.stage2 > 0 ? v.stage2 : v.stage1) + v.tile);
+  const double at_once = v.per_cu * cus, full = floor(items / at_once), rest = items - full * at_once;
+  double t = full * (stages * v.stage2 + v.tile);
   if (rest > 0) t += stages * (rest <= cus ? v.stage1 : v.stage2) + v.tile;
   t = t > memory ? t : memory;
-  if (splits > 1) t += 3.9 + 2 * items * v.tm * v.tn * 4 / 5.0e6;  // scaled_join, and its sums to memory and back
+  if (splits > 1) t += 3.4 + 2 * items * v.tm * v.tn * 4 / 5.2e6;  // scaled_join, and its sums to memory and back
   return t;
 }
 
 }  // namespace
 
-// The kernel that costs least: the figures are a fit to 260 products of 1 to
+// The kernel that costs least: the figures are a fit to 500 products of 1 to
 // 8192 rows, 64 to 8192 columns and K of 257 to 16384, each timed with every
-// kernel and up to ten splits; what it picks is 2.4% slower than the fastest
+// kernel and up to eight splits; what it picks is 2.5% slower than the fastest
 // of them on average.
 ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count) {
   // Short sums in exact products: with two K steps at most the time goes into
