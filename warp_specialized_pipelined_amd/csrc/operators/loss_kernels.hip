@@ -5,10 +5,10 @@
 // and its gradients, with g = (exp(logits - lse) - onehot(target)) dloss:
 //   dx = g w,   dw = g^T x.
 //
-// Forward: the GEMM's K loop makes 256 x 256 tiles of logits in registers;
-// each wave reduces its 128 columns of a row to a maximum and a sum of
-// exponentials, and a second kernel joins those of a row.  V / 128 pairs a
-// row are 1/32 of what bf16 logits would take.
+// Forward: tiles of logits are formed in registers; each wave reduces its
+// columns of a row (128 of them in a 256 x 256 tile) to a maximum and a sum of
+// exponentials, and a second kernel joins those of a row.  V / 128 pairs a row
+// are 1/32 of what bf16 logits would take.
 //
 // Backward: rows that do not count are left out first (x's other rows are
 // copied together), so they cost nothing and whatever they hold (a NaN in
@@ -16,13 +16,22 @@
 // logits are formed again, g of the piece is stored as bf16, and two products
 // read it: dw of the piece, complete, and the piece's share of dx, added up
 // in fp32.  g is the one quantity rounded to bf16 in between: the matrix
-// instructions take bf16 pairs; its rounding, half a step of 2^-8 a term and
-// independent from term to term, is of the size of the rounding of the
-// outputs themselves.
+// instructions take bf16 pairs.  It is stored as a multiple of the largest
+// |dloss|, and the products are scaled back in fp32: where dloss is the same
+// in every row, as for a mean, the one-hot part, which makes up nearly all of
+// g, is then exactly -1, and what is rounded (half a step, 2^-9 on average, of
+// each exp(logits - lse)) is far below the rounding of the outputs.
 //
-// Bound: the matrix instructions (one product forward, three backward).
+// The tiles are 256 x 256 with the GEMM's K loop, or 128 x 128 or 64 x 64
+// (midtile.hpp) where those are too few or too large; in the backward pass
+// the small tiles' two products share a launch and K is split.
+//
+// Bound: the matrix instructions (one product forward, three backward), or
+// for small ones launches and latency.
 #include <hip/hip_runtime.h>
 
+#include <stdio.h>
+#include <stdlib.h>
 #include <type_traits>
 
 #include "../kernel/epilogue.hpp"
@@ -30,6 +39,7 @@
 #include "../kernel/mainloop.hpp"
 #include "../kernel/params.hpp"
 #include "../kernel/scheduler.hpp"
+#include "midtile.hpp"
 #include "operators.h"
 #include "tile_store.hpp"
 
@@ -59,50 +69,56 @@ struct Ids {
 
 // ------------------------------------------------------------------- forward
 
-// The wave's 128 x 128 logits of rows m0.., columns n0..: per row the largest
-// and the sum of exponentials against it, over the columns below V; and the
-// target's logit where it is among them.
-__device__ __forceinline__ void reduce_logits(Accum& acc, const LossArgs& s, int64_t m0, int64_t n0,
+// The wave's 32 BM x 32 BN logits of rows m0.., columns n0..: per row the
+// largest and the sum of exponentials against it, over the columns below V;
+// and the target's logit where it is among them.
+template <int BM, int BN>
+__device__ __forceinline__ void reduce_logits(f32x16 (&v)[BM][BN], const LossArgs& s, int64_t m0, int64_t n0,
                                               int lane) {
+  constexpr int kCols = 32 * BN;
   const int64_t T = s.gemm.M, V = s.gemm.N;
   const int lr = lane & 31, half = lane >> 5;
   if (n0 >= V) return;
-  const int left = V - n0 < kWaveTile ? (int)(V - n0) : kWaveTile;
-  float2* part = s.parts + (n0 / kWaveTile) * s.part_rows;
+  const int left = V - n0 < kCols ? (int)(V - n0) : kCols;
+  float2* part = s.parts + (n0 / kCols) * s.part_rows;
+  int want[BM];  // the target's column here, or -1
 #pragma unroll
-  for (int bi = 0; bi < 4; ++bi) {
+  for (int bi = 0; bi < BM; ++bi) {
     const int64_t row = m0 + 32 * bi + lr;
-    if (left < kWaveTile) {
+    const int64_t at = row < T ? s.target[row] - n0 : -1;
+    want[bi] = at >= 0 && at < left ? (int)at : -1;
+  }
 #pragma unroll
-      for (int bj = 0; bj < 4; ++bj)
+  for (int bi = 0; bi < BM; ++bi) {
+    const int64_t row = m0 + 32 * bi + lr;
+    if (left < kCols) {
+#pragma unroll
+      for (int bj = 0; bj < BN; ++bj)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) >= left) acc.v[bi][bj][i] = -INFINITY;
+          if (32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) >= left) v[bi][bj][i] = -INFINITY;
     }
-    float m = acc.v[bi][0][0];
+    float m = v[bi][0][0];
 #pragma unroll
-    for (int bj = 0; bj < 4; ++bj)
+    for (int bj = 0; bj < BN; ++bj)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m = fmaxf(m, acc.v[bi][bj][i]);
+      for (int i = 0; i < 16; ++i) m = fmaxf(m, v[bi][bj][i]);
     m = fmaxf(m, __shfl_xor(m, 32, 64));
     const float ref = reference_of(m);
     float sum = 0.0f;
 #pragma unroll
-    for (int bj = 0; bj < 4; ++bj)
+    for (int bj = 0; bj < BN; ++bj)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum += exp_diff(acc.v[bi][bj][i], ref);
+      for (int i = 0; i < 16; ++i) sum += exp_diff(v[bi][bj][i], ref);
     sum += __shfl_xor(sum, 32, 64);
     if (row < T && half == 0) part[row] = {m, sum};
-    // (A row's target lies in one window of V / 128: the search is rare.)
-    const int64_t at = row < T ? s.target[row] - n0 : -1;
-    const bool here = at >= 0 && at < left;
-    if (__ballot(here) != 0) {
-      const int want = here ? (int)at : -1;
+    // (A row's target lies in one window of the vocabulary: the search is rare.)
+    if (__ballot(want[bi] >= 0) != 0) {
 #pragma unroll
-      for (int bj = 0; bj < 4; ++bj)
+      for (int bj = 0; bj < BN; ++bj)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) == want) s.target_logit[row] = acc.v[bi][bj][i];
+          if (32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) == want[bi]) s.target_logit[row] = v[bi][bj][i];
     }
   }
 }
@@ -117,38 +133,70 @@ __global__ __launch_bounds__(kThreads, 1) void loss_forward_tiles(LossArgs s) {
     const Ids id(lane, wave);
     mainloop<2, true, true>(acc, a, t.tm, t.tn, id.wave, id.lane, none);
     const Ids ie(lane, wave);
-    reduce_logits(acc, s, (int64_t)t.tm * kTileM + (ie.wave >> 1) * kWaveTile,
+    reduce_logits(acc.v, s, (int64_t)t.tm * kTileM + (ie.wave >> 1) * kWaveTile,
                   (int64_t)t.tn * kTileN + (ie.wave & 1) * kWaveTile, ie.lane);
   }
 }
 
-// A row's pairs joined: 16 rows a workgroup, 64 threads a row.
+// Waves a SIMD: what the ring leaves room for, or the accumulators.
+constexpr int mid_waves(int tm, int tn, int slots) {
+  return tm * tn <= 64 * 64 ? 4 : ((tm + tn) * 128 * slots <= 80 * 1024 ? 2 : 1);
+}
+
+template <int TM, int TN, int SLOTS>
+__global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_forward_mid(LossArgs s) {
+  typedef MidGeom<TM, TN, SLOTS> G;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const KernelArgs& a = s.gemm;
+  const MidTile t = mid_tile(persistent_slot(blockIdx.x, gridDim.x), (int)((a.M + TM - 1) / TM),
+                             (int)((a.N + TN - 1) / TN));
+  MidAccum<G::kBM, G::kBN> acc;
+  mid_loop<2, true, true, TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, 0,
+                                         (int)((a.K + 63) / 64), a.K);
+  reduce_logits(acc.v, s, (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM,
+                (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN, lane);
+}
+
+// A largest logit and the sum of exponentials against it (of them all).
+struct Pair {
+  float m, sum;
+};
+__device__ __forceinline__ Pair join(Pair a, Pair b) {
+  const float top = fmaxf(a.m, b.m), ref = reference_of(top);
+  // (The factors are chosen, not the terms: a NaN sum stays one.)
+  return {top, a.sum * (a.m == -INFINITY ? 0.0f : exp_diff(reference_of(a.m), ref)) +
+                   b.sum * (b.m == -INFINITY ? 0.0f : exp_diff(reference_of(b.m), ref))};
+}
+
+// A row's pairs joined: ROWS rows a workgroup, 1024 / ROWS threads a row (few
+// rows: more threads each, and more workgroups).
+template <int ROWS>
 __global__ __launch_bounds__(1024) void loss_join(LossArgs s) {
-  __shared__ float ms[64][17], ss[64][17];
-  const int r = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int64_t row = (int64_t)blockIdx.x * 16 + r;
-  const int64_t parts = (s.gemm.N + kWaveTile - 1) / kWaveTile;
-  float m = -INFINITY, sum = 0.0f;
-  if (row < s.gemm.M) {
-    for (int64_t p = group; p < parts; p += 64) {
-      const float2 x = s.parts[p * s.part_rows + row];
-      const float top = fmaxf(m, x.x), ref = reference_of(top);
-      // (The factors are chosen, not the terms: a NaN sum stays one.)
-      sum = sum * (m == -INFINITY ? 0.0f : exp_diff(reference_of(m), ref)) +
-            x.y * (x.x == -INFINITY ? 0.0f : exp_diff(reference_of(x.x), ref));
-      m = top;
+  constexpr int kGroups = 1024 / ROWS;
+  __shared__ Pair pairs[16][ROWS];
+  const int r = threadIdx.x % ROWS, group = threadIdx.x / ROWS;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + r;
+  const bool in = row < s.gemm.M;
+  const int64_t parts = (s.gemm.N + s.part_cols - 1) / s.part_cols;
+  Pair p = {-INFINITY, 0.0f};
+  for (int64_t first = group; first < parts; first += 4 * kGroups) {
+    float2 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = first + i * kGroups;
+      x[i] = in && at < parts ? s.parts[at * s.part_rows + row] : float2{-INFINITY, 0.0f};
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p = join(p, Pair{x[i].x, x[i].y});
   }
-  ms[group][r] = m;
-  ss[group][r] = sum;
+#pragma unroll
+  for (int d = ROWS; d < 64; d <<= 1) p = join(p, Pair{__shfl_xor(p.m, d, 64), __shfl_xor(p.sum, d, 64)});
+  if ((threadIdx.x & 63) < ROWS) pairs[threadIdx.x >> 6][r] = p;
   __syncthreads();
-  if (group == 0 && row < s.gemm.M) {
-    for (int i = 1; i < 64; ++i) m = fmaxf(m, ms[i][r]);
-    const float ref = reference_of(m);
-    sum = 0.0f;
-    for (int i = 0; i < 64; ++i)
-      if (ms[i][r] != -INFINITY || ss[i][r] != 0.0f) sum += ss[i][r] * exp_diff(reference_of(ms[i][r]), ref);
-    const float lse = ref + logf(sum);
+  if (threadIdx.x < ROWS && in) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) p = join(p, pairs[i][r]);
+    const float lse = reference_of(p.m) + logf(p.sum);
     s.lse[row] = lse;
     const int64_t t = s.target[row];
     s.loss[row] = t < 0 ? 0.0f : (t < s.gemm.N ? lse - s.target_logit[row] : NAN);
@@ -157,17 +205,60 @@ __global__ __launch_bounds__(1024) void loss_join(LossArgs s) {
 
 // ------------------------------------------------------------------ backward
 
-// The rows that count (0 <= target < V), numbered in order: place[row] is the
-// row's number or -1, from[number] the row.  One workgroup.
-__global__ __launch_bounds__(1024) void loss_number_rows(LossArgs s) {
+// The rows that count (0 <= target < V), numbered in order and copied
+// together: x, with what their gradient needs; zeros in dx for the others.
+// from[number] is the row.  Each workgroup takes `rows` consecutive rows, and
+// counts the targets before them itself; the first one also counts them all
+// and finds the largest |dloss|.  A wave copies a row.
+__global__ __launch_bounds__(1024) void loss_gather_rows(LossArgs s, int64_t rows) {
   __shared__ int totals[16];
+  __shared__ float tops[16];
+  __shared__ int places[1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t begin = (int64_t)blockIdx.x * rows;
+  const int64_t end = begin + rows < s.T ? begin + rows : s.T;
+  auto counts = [&](int64_t t) { return t >= 0 && t < s.V; };
+  auto add_up = [&](int n) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d, 64);
+    if (lane == 0) totals[wave] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) n += totals[w];
+    __syncthreads();
+    return n;
+  };
+  if (blockIdx.x == 0) {
+    int n = 0;
+    float top = 0.0f;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < s.T; i += 1024) {
+      const float d = fabsf(s.dloss[i]);
+      if (counts(s.target[i])) {
+        ++n;
+        if (d < INFINITY) top = fmaxf(top, d);  // (neither infinity nor NaN)
+      }
+    }
+    n = add_up(n);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w]);
+      s.head->count = n;
+      s.head->top = top > 0.0f ? top : 1.0f;
+    }
+  }
   int base = 0;
-  for (int64_t first = 0; first < s.T; first += 1024) {
-    const int64_t row = first + threadIdx.x;
-    const int64_t t = row < s.T ? s.target[row] : -1;
-    const bool counts = t >= 0 && t < s.V;
-    const uint64_t mask = __ballot(counts);
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < begin; i += 1024) base += counts(s.target[i]);
+  base = add_up(base);
+  for (int64_t first = begin; first < end; first += 1024) {
+    const int64_t own = first + threadIdx.x;
+    const int64_t t = own < end ? s.target[own] : -1;
+    const uint64_t mask = __ballot(counts(t));
     if (lane == 0) totals[wave] = __popcll(mask);
     __syncthreads();
     int at = base + __popcll(mask & (((uint64_t)1 << lane) - 1));
@@ -175,46 +266,41 @@ __global__ __launch_bounds__(1024) void loss_number_rows(LossArgs s) {
       if (w < wave) at += totals[w];
       base += totals[w];
     }
-    if (row < s.T) s.place[row] = counts ? at : -1;
-    if (counts) s.from[at] = (int)row;
+    places[threadIdx.x] = counts(t) ? at : -1;
+    if (counts(t)) {
+      s.from[at] = (int)own;
+      s.rows_lse[at] = s.lse[own];
+      s.rows_dloss[at] = s.dloss[own];
+      s.rows_target[at] = (int)t;
+    }
     __syncthreads();
-  }
-  if (threadIdx.x == 0) *s.count = base;
-}
-
-// Row by row: x of the rows that count copied together, with what their
-// gradient needs; zeros in dx for the others.  A wave takes a row.
-__global__ __launch_bounds__(256) void loss_gather_rows(LossArgs s) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < s.T; row += (int64_t)gridDim.x * 4) {
-    const int at = s.place[row];
-    if (at >= 0) {
-      // (Whole 16-byte blocks: the last one's bytes past H are never used.)
-      const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const unsigned short*>(s.x) + row * s.x_rs);
-      u32x4* to = reinterpret_cast<u32x4*>(s.rows_x + (int64_t)at * s.rows_ld);
-      for (int64_t c = lane; c * 8 < s.H; c += 64) to[c] = from[c];
-      if (lane == 0) {
-        s.rows_lse[at] = s.lse[row];
-        s.rows_dloss[at] = s.dloss[row];
-        s.rows_target[at] = (int)s.target[row];
-      }
-    } else {
-      unsigned short* d = static_cast<unsigned short*>(s.dx) + row * s.dx_rs;
-      for (int64_t c = (int64_t)lane * 8; c < s.H; c += 512) {
-        if (c + 8 <= s.H) {
-          *reinterpret_cast<u32x4*>(d + c) = u32x4{0, 0, 0, 0};
-        } else {
-          for (int e = 0; c + e < s.H; ++e) d[c + e] = 0;
+    for (int i = wave; i < 1024 && first + i < end; i += 16) {
+      const int64_t row = first + i;
+      const int place = places[i];
+      if (place >= 0) {
+        // (Whole 16-byte blocks: the last one's bytes past H are never used.)
+        const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const unsigned short*>(s.x) + row * s.x_rs);
+        u32x4* to = reinterpret_cast<u32x4*>(s.rows_x + (int64_t)place * s.rows_ld);
+#pragma unroll 4
+        for (int64_t c = lane; c * 8 < s.H; c += 64) to[c] = from[c];
+      } else {
+        unsigned short* d = static_cast<unsigned short*>(s.dx) + row * s.dx_rs;
+        for (int64_t c = (int64_t)lane * 8; c < s.H; c += 512) {
+          if (c + 8 <= s.H) {
+            *reinterpret_cast<u32x4*>(d + c) = u32x4{0, 0, 0, 0};
+          } else {
+            for (int e = 0; c + e < s.H; ++e) d[c + e] = 0;
+          }
         }
       }
     }
+    __syncthreads();  // places and totals are read before the next rows' are written
   }
 }
 
 // The arguments of a product whose rows (M) are the rows that count.
-__device__ __forceinline__ KernelArgs with_rows(const LossArgs& s) {
-  KernelArgs a = s.gemm;
-  const int count = *s.count;
+__device__ __forceinline__ KernelArgs with_rows(const LossArgs& s, KernelArgs a) {
+  const int count = s.head->count;
   a.M = count;
   a.a_bytes = count > 0 ? ((int64_t)(count - 1) * a.lda + a.K) * 2 : 0;
   a.tiles_m = (count + kTileM - 1) / kTileM;
@@ -223,10 +309,45 @@ __device__ __forceinline__ KernelArgs with_rows(const LossArgs& s) {
   return a;
 }
 
-// g of one piece of the vocabulary: columns first_col .. + N.
+// The wave's logits of rows m0.., columns n0.. of the piece (first_col ..) made
+// g, as a multiple of the largest |dloss|.
+template <int BM, int BN>
+__device__ __forceinline__ void logits_to_gradient(f32x16 (&v)[BM][BN], const LossArgs& s, int64_t rows,
+                                                   int64_t m0, int64_t n0, int lane) {
+  const int lr = lane & 31, half = lane >> 5;
+  const float top = s.head->top;
+  float lse[BM], scale[BM];
+  int want[BM];  // the target's column here, or -1
+#pragma unroll
+  for (int bi = 0; bi < BM; ++bi) {
+    const int64_t row = m0 + 32 * bi + lr;
+    const bool in = row < rows;
+    lse[bi] = in ? s.rows_lse[row] : 0.0f;
+    scale[bi] = in ? s.rows_dloss[row] / top : 0.0f;
+    const int64_t at = in ? (int64_t)s.rows_target[row] - s.first_col - n0 : -1;
+    want[bi] = at >= 0 && at < 32 * BN ? (int)at : -1;
+  }
+#pragma unroll
+  for (int bi = 0; bi < BM; ++bi) {
+    const bool search = __ballot(want[bi] >= 0) != 0;
+#pragma unroll
+    for (int bj = 0; bj < BN; ++bj)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float p = exp_diff(v[bi][bj][i], lse[bi]);
+        if (search && 32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) == want[bi]) p -= 1.0f;
+        v[bi][bj][i] = p * scale[bi];
+      }
+  }
+}
+__device__ __forceinline__ f32x4 quarter_of(const f32x16& v, int q) {
+  return f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+}
+
+// g of one piece of the vocabulary.
 __global__ __launch_bounds__(kThreads, 1) void loss_gradient_tiles(LossArgs s) {
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const KernelArgs a = with_rows(s);
+  const KernelArgs a = with_rows(s, s.gemm);
   Accum acc;
   NoSideWork none;
   for (int L = persistent_slot(blockIdx.x, gridDim.x); L < a.num_tiles; L += gridDim.x) {
@@ -236,32 +357,31 @@ __global__ __launch_bounds__(kThreads, 1) void loss_gradient_tiles(LossArgs s) {
     const Ids ie(lane, wave);
     const int64_t m0 = (int64_t)t.tm * kTileM + (ie.wave >> 1) * kWaveTile;
     const int64_t n0 = (int64_t)t.tn * kTileN + (ie.wave & 1) * kWaveTile;
-    const int lr = ie.lane & 31, half = ie.lane >> 5;
-#pragma unroll
-    for (int bi = 0; bi < 4; ++bi) {
-      const int64_t row = m0 + 32 * bi + lr;
-      const bool in = row < a.M;
-      const float lse = in ? s.rows_lse[row] : 0.0f, dl = in ? s.rows_dloss[row] : 0.0f;
-      const int64_t at = in ? (int64_t)s.rows_target[row] - s.first_col - n0 : -1;
-      const bool here = at >= 0 && at < kWaveTile;
-      const int want = here ? (int)at : -1;
-      const bool search = __ballot(here) != 0;
-#pragma unroll
-      for (int bj = 0; bj < 4; ++bj)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float p = exp_diff(acc.v[bi][bj][i], lse);
-          if (search && 32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) == want) p -= 1.0f;
-          acc.v[bi][bj][i] = p * dl;
-        }
-    }
-    tile_store<false>(a.D, a.ldd, a.M, a.N, m0, n0, ie.wave, ie.lane, [&](int bi, int bj, int q) {
-      const f32x16& v = acc.v[bi][bj];
-      return f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-    });
+    logits_to_gradient(acc.v, s, a.M, m0, n0, ie.lane);
+    tile_store<false>(a.D, a.ldd, a.M, a.N, m0, n0, ie.wave, ie.lane,
+                      [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q); });
     wait_lgkmcnt<0>();  // staging reads done ...
     barrier();          // ... in every wave before the ring is refilled
   }
+}
+
+template <int TM, int TN, int SLOTS>
+__global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_gradient_mid(LossArgs s) {
+  typedef MidGeom<TM, TN, SLOTS> G;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const MidTile t = mid_tile(persistent_slot(blockIdx.x, gridDim.x), (int)((s.gemm.M + TM - 1) / TM),
+                             (int)((s.gemm.N + TN - 1) / TN));
+  const KernelArgs a = with_rows(s, s.gemm);
+  if ((int64_t)t.tm * TM >= a.M) return;
+  MidAccum<G::kBM, G::kBN> acc;
+  mid_loop<2, true, true, TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, 0,
+                                         (int)((a.K + 63) / 64), a.K);
+  const int64_t m0 = (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM;
+  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN;
+  logits_to_gradient(acc.v, s, a.M, m0, n0, lane);
+  mid_store<G::kBM, G::kBN>(
+      a.D, a.ldd, a.M, a.N, m0, n0, wave, lane,
+      [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q); }, [](int64_t r) { return r; });
 }
 
 // dw of the piece = g^T x: rows are the piece's vocabulary, K the rows that
@@ -269,7 +389,8 @@ __global__ __launch_bounds__(kThreads, 1) void loss_gradient_tiles(LossArgs s) {
 __global__ __launch_bounds__(kThreads, 1) void loss_dw_tiles(LossArgs s) {
   const int lane = threadIdx.x & 63, wave = wave_id();
   KernelArgs a = s.gemm;
-  const int count = *s.count;
+  const int count = s.head->count;
+  const float top = s.head->top;
   a.K = count;
   a.a_bytes = count > 0 ? ((int64_t)(count - 1) * a.lda + a.M) * 2 : 0;
   a.b_bytes = count > 0 ? ((int64_t)(count - 1) * a.ldb + a.N) * 2 : 0;
@@ -282,17 +403,14 @@ __global__ __launch_bounds__(kThreads, 1) void loss_dw_tiles(LossArgs s) {
     const Ids ie(lane, wave);
     tile_store<true>(a.D, a.ldd, a.M, a.N, (int64_t)t.tm * kTileM + (ie.wave >> 1) * kWaveTile,
                      (int64_t)t.tn * kTileN + (ie.wave & 1) * kWaveTile, ie.wave, ie.lane,
-                     [&](int bi, int bj, int q) {
-                       const f32x16& v = acc.v[bi][bj];
-                       return f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-                     });
+                     [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * top; });
     wait_lgkmcnt<0>();
     barrier();
   }
 }
 
-// A wave's 16 KiB-per-row-block share of a tile's fp32 sums in register
-// order: piece (block b, quarter q) of lane l at ((4 b + q) * 64 + l) * 16.
+// A wave's share of a 256 x 256 tile's fp32 sums in register order: piece
+// (block b, quarter q) of lane l at ((4 b + q) * 64 + l) * 16.
 __device__ __forceinline__ f32x4* dx_pieces(const LossArgs& s, int split, int64_t tile, int wave) {
   return s.dx_sums + ((split * s.dx_tiles + tile) * kWaves + wave) * (kWaveTile * kWaveTile / 4);
 }
@@ -301,7 +419,7 @@ __device__ __forceinline__ f32x4* dx_pieces(const LossArgs& s, int split, int64_
 // its own sums (the first piece of the vocabulary sets them).
 __global__ __launch_bounds__(kThreads, 1) void loss_dx_tiles(LossArgs s) {
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const KernelArgs a = with_rows(s);
+  const KernelArgs a = with_rows(s, s.gemm);
   const int stages = (int)((a.K + 63) / 64);
   const int items = a.num_tiles * s.splits;
   Accum acc;
@@ -339,7 +457,8 @@ __global__ __launch_bounds__(256) void loss_dx_finish(LossArgs s) {
   const int64_t tm = tile / tiles_n, tn = tile % tiles_n;
   const int lane = threadIdx.x & 63, bj = threadIdx.x >> 6;
   const int64_t row = tm * kTileM + (wave >> 1) * kWaveTile + 32 * bi + (lane & 31);
-  if (row >= *s.count) return;
+  if (row >= s.head->count) return;
+  const float top = s.head->top;
   unsigned short* d = static_cast<unsigned short*>(s.dx) + (int64_t)s.from[row] * s.dx_rs;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -347,64 +466,201 @@ __global__ __launch_bounds__(256) void loss_dx_finish(LossArgs s) {
     if (c >= s.H) continue;
     f32x4 x = {0, 0, 0, 0};
     for (int i = 0; i < s.splits; ++i) x += dx_pieces(s, i, tile, wave)[(4 * (4 * bi + bj) + q) * 64 + lane];
-    const u32x2 w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
-    if (c + 4 <= s.H) {
-      *reinterpret_cast<u32x2*>(d + c) = w;
+    store4(d + c, s.H - c, x * top);
+  }
+}
+
+// The small tiles' two products, in one launch: workgroups 0 .. are the parts
+// of dx (K split dx_splits ways), those after them the parts of dw.  A product
+// that one workgroup finishes is stored at once; else the sums go to memory in
+// register order (those of dx are added to from piece to piece) and
+// loss_finish_mid adds them up.
+template <int TM, int TN, int SLOTS>
+__global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_mid(LossArgs s) {
+  typedef MidGeom<TM, TN, SLOTS> G;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int count = s.head->count;
+  const float top = s.head->top;
+  const int dx_tiles_m = (int)((s.T + TM - 1) / TM), tiles_n = (int)((s.H + TN - 1) / TN);
+  const int dx_tiles = dx_tiles_m * tiles_n, dx_items = dx_tiles * s.splits;
+  const int slot = persistent_slot(blockIdx.x, gridDim.x);
+  MidAccum<G::kBM, G::kBN> acc;
+  if (slot < dx_items) {
+    const KernelArgs a = with_rows(s, s.gemm_dx);
+    const int split = slot / dx_tiles;
+    const MidTile t = mid_tile(slot - split * dx_tiles, dx_tiles_m, tiles_n);
+    if ((int64_t)t.tm * TM >= a.M) return;
+    const int stages = (int)((a.K + 63) / 64);
+    const int k0 = (int)((int64_t)stages * split / s.splits), k1 = (int)((int64_t)stages * (split + 1) / s.splits);
+    const int64_t kend = (int64_t)k1 * 64 < a.K ? (int64_t)k1 * 64 : a.K;
+    mid_loop<2, true, false, TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0, k1 - k0,
+                                            kend);
+    if (s.dx_summed) {
+      if (!s.first_piece) mid_add_all(s.dx_sums, slot, acc, wave, lane);
+      mid_put(s.dx_sums, slot, acc, wave, lane);
     } else {
-      for (int e = 0; e < (int)(s.H - c); ++e) d[c + e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+      mid_store<G::kBM, G::kBN>(
+          a.D, a.ldd, a.M, a.N, (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM,
+          (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN, wave, lane,
+          [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * top; },
+          [&](int64_t r) { return (int64_t)s.from[r]; });
+    }
+  } else {
+    KernelArgs a = s.gemm;
+    a.K = count;
+    a.a_bytes = count > 0 ? ((int64_t)(count - 1) * a.lda + a.M) * 2 : 0;
+    a.b_bytes = count > 0 ? ((int64_t)(count - 1) * a.ldb + a.N) * 2 : 0;
+    const int tiles_m = (int)((a.M + TM - 1) / TM), tiles = tiles_m * tiles_n;
+    const int split = (slot - dx_items) / tiles;
+    const MidTile t = mid_tile(slot - dx_items - split * tiles, tiles_m, tiles_n);
+    const int stages = (count + 63) / 64;
+    const int k0 = (int)((int64_t)stages * split / s.dw_splits);
+    const int k1 = (int)((int64_t)stages * (split + 1) / s.dw_splits);
+    mid_loop<2, false, false, TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0,
+                                             k1 - k0, k1 * 64 < count ? k1 * 64 : count);
+    if (s.dw_splits > 1) {
+      mid_put(s.dw_sums, slot - dx_items, acc, wave, lane);
+    } else {
+      mid_store<G::kBM, G::kBN>(
+          a.D, a.ldd, a.M, a.N, (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM,
+          (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN, wave, lane,
+          [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * top; }, [](int64_t r) { return r; });
     }
   }
 }
 
+// The sums of one 32 x 32 block of dx (the first dx_blocks workgroups) or dw,
+// added in the order of the splits, scaled and stored.
+template <int TM, int TN>
+__global__ __launch_bounds__(64) void loss_finish_mid(LossArgs s, int dx_blocks) {
+  constexpr int BM = TM / 64, BN = TN / 64;
+  const int lane = threadIdx.x;
+  const bool dx = (int)blockIdx.x < dx_blocks;
+  const int at = dx ? blockIdx.x : blockIdx.x - dx_blocks;
+  const int64_t M = dx ? s.head->count : s.gemm.M;
+  const int tiles_m = (int)(((dx ? s.T : M) + TM - 1) / TM), tiles_n = (int)((s.H + TN - 1) / TN);
+  const int part = at % (4 * BM * BN), tile = at / (4 * BM * BN);
+  const int wave = part / (BM * BN), block = part % (BM * BN);
+  const MidTile t = mid_tile(tile, tiles_m, tiles_n);
+  const int64_t m = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM + 32 * (block / BN) + (lane & 31);
+  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN + 32 * (block % BN);
+  if (m >= M || n0 >= s.H) return;
+  const float top = s.head->top;
+  MidAccum<1, 1> acc = {};
+  const int splits = dx ? s.splits : s.dw_splits;
+  const mid_piece* sums = dx ? s.dx_sums : s.dw_sums;
+#pragma unroll 4
+  for (int i = 0; i < splits; ++i) mid_add<BM, BN>(sums, (int64_t)i * tiles_m * tiles_n + tile, acc, wave, block, lane);
+  unsigned short* d = dx ? static_cast<unsigned short*>(s.dx) + (int64_t)s.from[m] * s.dx_rs
+                         : static_cast<unsigned short*>(s.gemm.D) + m * s.gemm.ldd;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t n = n0 + 8 * q + 4 * (lane >> 5);
+    store4(d + n, s.H - n, quarter_of(acc.v[0][0], q) * top);
+  }
+}
+
+typedef void (*loss_fn)(LossArgs);
+struct MidKernels {
+  int lds;
+  loss_fn forward, gradient, products;
+  void (*finish)(LossArgs, int);
+};
+template <int TM, int TN, int SLOTS>
+constexpr MidKernels mid_kernels() {
+  return {(int)MidGeom<TM, TN, SLOTS>::kLds, loss_forward_mid<TM, TN, SLOTS>, loss_gradient_mid<TM, TN, SLOTS>,
+          loss_products_mid<TM, TN, SLOTS>, loss_finish_mid<TM, TN>};
+}
+const MidKernels kMid[] = {mid_kernels<128, 128, 4>(), mid_kernels<64, 64, 4>(), mid_kernels<64, 128, 3>(), mid_kernels<128, 128, 2>()};  // from kLoss128 on
+
 }  // namespace
 
+LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_count) {
+  LossChoice c = {0, 0, 0, 1, 1};
+  const int64_t stages = ((piece < V ? piece : V) + 63) / 64, dx_tiles = loss_tiles(kLoss256, T, H);
+  int64_t splits = dx_tiles > 0 ? cu_count / dx_tiles : 1;
+  splits = splits > stages / 8 ? stages / 8 : splits;
+  c.dx_splits = splits < 1 ? 1 : (int)splits;
+  if (const char* e = getenv("MIGEMM_L"))
+    sscanf(e, "%d,%d,%d,%d,%d", &c.forward, &c.gradient, &c.products, &c.dx_splits, &c.dw_splits);
+  return c;
+}
+
 hipError_t prepare_loss() {
-  const void* f[] = {reinterpret_cast<const void*>(loss_forward_tiles),
-                     reinterpret_cast<const void*>(loss_gradient_tiles),
-                     reinterpret_cast<const void*>(loss_dw_tiles),
-                     reinterpret_cast<const void*>(loss_dx_tiles)};
-  for (const void* k : f) {
-    const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kPlainLdsBytes);
+  struct {
+    loss_fn f;
+    int lds;
+  } all[16] = {{loss_forward_tiles, kPlainLdsBytes}, {loss_gradient_tiles, kPlainLdsBytes},
+               {loss_dw_tiles, kPlainLdsBytes}, {loss_dx_tiles, kPlainLdsBytes}};
+  int n = 4;
+  for (const MidKernels& m : kMid)
+    for (loss_fn f : {m.forward, m.gradient, m.products}) all[n++] = {f, m.lds};
+  for (int i = 0; i < n; ++i) {
+    const auto& k = all[i];
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k.f),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, k.lds);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-#define MIGEMM_LAUNCH(kernel, grid, threads, lds)                                            \
+#define MIGEMM_LAUNCH(kernel, grid, threads, lds, ...)                                          \
   do {                                                                                       \
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(grid)), dim3(threads), lds, stream, s);       \
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(grid)), dim3(threads), lds, stream, __VA_ARGS__); \
     const hipError_t e = hipGetLastError();                                                  \
     if (e != hipSuccess) return e;                                                           \
   } while (0)
 
-hipError_t launch_loss_forward(const LossArgs& s, int grid, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_forward_tiles, grid, kThreads, kPlainLdsBytes);
-  MIGEMM_LAUNCH(loss_join, (s.gemm.M + 15) / 16, 1024, 0);
+hipError_t launch_loss_forward(const LossArgs& s, int tile, int cu_count, hipStream_t stream) {
+  const int64_t tiles = loss_tiles(tile, s.gemm.M, s.gemm.N);
+  if (tile == kLoss256) {
+    MIGEMM_LAUNCH(loss_forward_tiles, tiles < cu_count ? tiles : cu_count, kThreads, kPlainLdsBytes, s);
+  } else {
+    MIGEMM_LAUNCH(kMid[tile - 1].forward, tiles, 256, kMid[tile - 1].lds, s);
+  }
+  // Few rows: 4 a workgroup.
+  if (s.gemm.M <= 2048) MIGEMM_LAUNCH(loss_join<4>, (s.gemm.M + 3) / 4, 1024, 0, s);
+  else MIGEMM_LAUNCH(loss_join<16>, (s.gemm.M + 15) / 16, 1024, 0, s);
   return hipSuccess;
 }
 
 hipError_t launch_loss_rows(const LossArgs& s, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_number_rows, 1, 1024, 0);
-  if (s.T > 0) {
-    const int64_t grid = (s.T + 3) / 4;
-    MIGEMM_LAUNCH(loss_gather_rows, grid < 65536 ? grid : 65536, 256, 0);
+  int64_t grid = (s.T + 3) / 4;
+  grid = grid < 1 ? 1 : (grid > 256 ? 256 : grid);
+  MIGEMM_LAUNCH(loss_gather_rows, grid, 1024, 0, s, (s.T + grid - 1) / grid);
+  return hipSuccess;
+}
+hipError_t launch_loss_gradient(const LossArgs& s, int tile, int cu_count, hipStream_t stream) {
+  const int64_t tiles = loss_tiles(tile, s.gemm.M, s.gemm.N);
+  if (tile == kLoss256) {
+    MIGEMM_LAUNCH(loss_gradient_tiles, tiles < cu_count ? tiles : cu_count, kThreads, kPlainLdsBytes, s);
+  } else {
+    MIGEMM_LAUNCH(kMid[tile - 1].gradient, tiles, 256, kMid[tile - 1].lds, s);
   }
   return hipSuccess;
 }
-hipError_t launch_loss_gradient(const LossArgs& s, int grid, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_gradient_tiles, grid, kThreads, kPlainLdsBytes);
+hipError_t launch_loss_dw(const LossArgs& s, int cu_count, hipStream_t stream) {
+  MIGEMM_LAUNCH(loss_dw_tiles, s.gemm.num_tiles < cu_count ? s.gemm.num_tiles : cu_count, kThreads,
+                kPlainLdsBytes, s);
   return hipSuccess;
 }
-hipError_t launch_loss_dw(const LossArgs& s, int grid, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_dw_tiles, grid, kThreads, kPlainLdsBytes);
-  return hipSuccess;
-}
-hipError_t launch_loss_dx(const LossArgs& s, int grid, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_dx_tiles, grid, kThreads, kPlainLdsBytes);
+hipError_t launch_loss_dx(const LossArgs& s, int cu_count, hipStream_t stream) {
+  const int64_t items = (int64_t)s.gemm.num_tiles * s.splits;
+  MIGEMM_LAUNCH(loss_dx_tiles, items < cu_count ? items : cu_count, kThreads, kPlainLdsBytes, s);
   return hipSuccess;
 }
 hipError_t launch_loss_dx_finish(const LossArgs& s, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_dx_finish, s.dx_tiles * 16, 256, 0);
+  MIGEMM_LAUNCH(loss_dx_finish, s.dx_tiles * 16, 256, 0, s);
+  return hipSuccess;
+}
+hipError_t launch_loss_products(const LossArgs& s, int tile, bool last_piece, hipStream_t stream) {
+  const int blocks = (kLossTileM[tile] / 32) * (kLossTileN[tile] / 32);
+  const MidKernels& m = kMid[tile - 1];
+  const int64_t dw_tiles = loss_tiles(tile, s.gemm.M, s.H);
+  MIGEMM_LAUNCH(m.products, s.dx_tiles * s.splits + dw_tiles * s.dw_splits, 256, m.lds, s);
+  const int64_t dx_blocks = s.dx_summed && last_piece ? s.dx_tiles * blocks : 0;
+  const int64_t dw_blocks = s.dw_splits > 1 ? dw_tiles * blocks : 0;
+  if (dx_blocks + dw_blocks > 0) MIGEMM_LAUNCH(m.finish, dx_blocks + dw_blocks, 64, 0, s, (int)dx_blocks);
   return hipSuccess;
 }
 

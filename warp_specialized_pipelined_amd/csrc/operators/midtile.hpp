@@ -329,6 +329,20 @@ __device__ __forceinline__ void mid_put(mid_piece* sums, int64_t item, const Mid
       p[(4 * b + q) * 64] = mid_piece{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
     }
 }
+// Adds such sums to acc.
+template <int BM, int BN>
+__device__ __forceinline__ void mid_add_all(const mid_piece* sums, int64_t item, MidAccum<BM, BN>& acc, int wave,
+                                            int lane) {
+  const mid_piece* p = sums + ((item * 4 + wave) * BM * BN) * 256 + lane;
+#pragma unroll
+  for (int b = 0; b < BM * BN; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const mid_piece x = p[(4 * b + q) * 64];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc.v[b / BN][b % BN][4 * q + c] += x[c];
+    }
+}
 // Adds one block of such sums to acc.
 template <int BM, int BN>
 __device__ __forceinline__ void mid_add(const mid_piece* sums, int64_t item, MidAccum<1, 1>& acc, int wave,

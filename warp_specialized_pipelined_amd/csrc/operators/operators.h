@@ -71,11 +71,15 @@ hipError_t launch_scaled(const ScaledArgs& a, int variant, int cu_count, hipStre
 
 // ------------------------------------------------------------------- loss
 
-// Four fp32 sums of dx.
-typedef float dx_piece __attribute__((ext_vector_type(4)));
+// What the backward pass finds out about its rows.
+struct LossHead {
+  int count;  // rows that count
+  float top;  // the largest |dloss| of theirs, or 1
+};
 
 struct LossArgs {
   KernelArgs gemm;        // the product a kernel forms
+  KernelArgs gemm_dx;     // loss_products_mid: dx's, beside dw's
   int64_t T, V, H;
   const void* x;          // the caller's, T x H
   int64_t x_rs, dx_rs;
@@ -84,33 +88,53 @@ struct LossArgs {
   // gemm.M rows that a launch takes.)
   float* loss;
   float* lse;             // backward: in
-  float2* parts;          // [V / 128][part_rows]: largest logit, sum of exponentials
-  int64_t part_rows;
+  float2* parts;          // [V / part_cols][part_rows]: largest logit, sum of exponentials
+  int64_t part_rows, part_cols;
   float* target_logit;
   // Backward.
   const float* dloss;
   void* dx;
-  int* count;             // rows that count
-  int* place;             // [T]
-  int* from;              // [count]
+  LossHead* head;
+  int* from;              // [count]: the row's number among T
   unsigned short* rows_x; // [count][rows_ld]
   int64_t rows_ld;
   float* rows_lse;
   float* rows_dloss;
   int* rows_target;
   int64_t first_col;      // the piece's first vocabulary entry
-  dx_piece* dx_sums;    // [splits][dx_tiles] tiles of fp32 sums in register order
+  mid_piece* dx_sums;     // [splits][dx_tiles] tiles of fp32 sums in register order
+  mid_piece* dw_sums;     // [dw_splits][tiles of dw]
   int64_t dx_tiles;
-  int32_t splits;
-  int32_t first_piece;
+  int32_t splits, dw_splits;
+  int32_t first_piece, dx_summed;
 };
 
+// Tiles of the loss's products: 256 x 256 (the GEMM's K loop) or smaller
+// (midtile.hpp).
+enum LossTile { kLoss256, kLoss128, kLoss64, kLoss64x128, kLoss128b };
+constexpr int kLossTileM[] = {256, 128, 64, 64, 128};
+constexpr int kLossTileN[] = {256, 128, 64, 128, 128};
+inline int64_t loss_tiles(int tile, int64_t rows, int64_t cols) {
+  return ((rows + kLossTileM[tile] - 1) / kLossTileM[tile]) * ((cols + kLossTileN[tile] - 1) / kLossTileN[tile]);
+}
+
+// The tiles of the logits forward and backward and of the backward pass's
+// products, and the ways K of those is split.  `piece`: vocabulary entries
+// that the backward pass takes at a time.
+struct LossChoice {
+  int forward, gradient, products, dx_splits, dw_splits;
+};
+LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_count);
+
 hipError_t prepare_loss();
-hipError_t launch_loss_forward(const LossArgs& s, int grid, hipStream_t stream);
+hipError_t launch_loss_forward(const LossArgs& s, int tile, int cu_count, hipStream_t stream);
 hipError_t launch_loss_rows(const LossArgs& s, hipStream_t stream);
-hipError_t launch_loss_gradient(const LossArgs& s, int grid, hipStream_t stream);
-hipError_t launch_loss_dw(const LossArgs& s, int grid, hipStream_t stream);
-hipError_t launch_loss_dx(const LossArgs& s, int grid, hipStream_t stream);
+hipError_t launch_loss_gradient(const LossArgs& s, int tile, int cu_count, hipStream_t stream);
+// 256 x 256 tiles: dw, dx, and after the last piece what dx's sums come to.
+hipError_t launch_loss_dw(const LossArgs& s, int cu_count, hipStream_t stream);
+hipError_t launch_loss_dx(const LossArgs& s, int cu_count, hipStream_t stream);
 hipError_t launch_loss_dx_finish(const LossArgs& s, hipStream_t stream);
+// Smaller tiles: both, and what is summed of them.
+hipError_t launch_loss_products(const LossArgs& s, int tile, bool last_piece, hipStream_t stream);
 
 }  // namespace migemm

@@ -23,11 +23,12 @@ struct migemm_vocab_loss_plan {
   int cus;
   // Forward: rows a launch takes (the workspace holds one launch's pairs).
   int64_t chunk;
-  // Backward: vocabulary entries a piece, g's row stride, the ways K of dx is
-  // split, and where things lie in the workspace.
+  // Backward: vocabulary entries a piece, g's row stride, and where things
+  // lie in the workspace.
   int64_t piece, g_rs, rows_rs, dx_tiles;
-  int splits;
-  size_t at_place, at_from, at_lse, at_dloss, at_target, at_rows, at_g, at_sums;
+  migemm::LossChoice choice;
+  bool dx_summed;
+  size_t at_from, at_lse, at_dloss, at_target, at_rows, at_g, at_dx, at_dw;
   size_t workspace_bytes;
 };
 
@@ -216,36 +217,36 @@ void lay_out_loss(migemm_vocab_loss_plan* p) {
   const migemm_vocab_loss_desc& d = p->desc;
   const int64_t T = d.rows, V = d.vocab, H = d.hidden;
   p->chunk = T < kLossChunk ? T : kLossChunk;
-  const int64_t parts = (V + migemm::kWaveTile - 1) / migemm::kWaveTile;
-  p->workspace_bytes = (size_t)(parts * p->chunk * 8 + p->chunk * 4);
-  if (d.dx_rs == 0) return;
   // Pieces of g within kPieceBytes, of equal width.
   int64_t most = kPieceBytes / 2 / up(T > 0 ? T : 1, 256) / 256 * 256;
   most = most < 1024 ? 1024 : (most > (1 << 20) ? 1 << 20 : most);
   const int64_t pieces = (V + most - 1) / most;
   p->piece = up((V + pieces - 1) / pieces, 256);
-  p->g_rs = up(p->piece < V ? p->piece : V, 64) + 64;  // rows not a power of two apart
+  p->choice = migemm::choose_loss(T, V, H, p->piece, p->cus);
+  const migemm::LossChoice& c = p->choice;
+  const int64_t part_cols = migemm::kLossTileN[c.forward] / 2;
+  p->workspace_bytes = (size_t)((V + part_cols - 1) / part_cols * p->chunk * 8 + p->chunk * 4);
+  if (d.dx_rs == 0) return;
+  const int64_t width = p->piece < V ? p->piece : V;
+  p->g_rs = up(width, 64) + 64;  // rows not a power of two apart
   p->rows_rs = up(H, 64);
-  const int64_t tiles_m = (T + 255) / 256, tiles_n = (H + 255) / 256;
-  p->dx_tiles = tiles_m * tiles_n;
-  const int64_t stages = ((p->piece < V ? p->piece : V) + 63) / 64;
-  int64_t splits = p->dx_tiles > 0 ? p->cus / p->dx_tiles : 1;
-  splits = splits > stages ? stages : splits;
-  p->splits = (int)(splits < 1 ? 1 : splits);
-  size_t at = 256;  // the count
+  const int64_t tile_bytes = 4 * migemm::kLossTileM[c.products] * migemm::kLossTileN[c.products];
+  p->dx_tiles = migemm::loss_tiles(c.products, T, H);
+  p->dx_summed = c.products == migemm::kLoss256 || c.dx_splits > 1 || p->piece < V;
+  size_t at = 256;  // the head
   auto take = [&](int64_t bytes) {
     const size_t from = at;
     at += (size_t)up(bytes, 256);
     return from;
   };
-  p->at_place = take(T * 4);
   p->at_from = take(T * 4);
   p->at_lse = take(T * 4);
   p->at_dloss = take(T * 4);
   p->at_target = take(T * 4);
   p->at_rows = take(T * p->rows_rs * 2);
   p->at_g = take(T * p->g_rs * 2);
-  p->at_sums = take(p->splits * p->dx_tiles * migemm::kTileM * migemm::kTileN * 4);
+  p->at_dx = take(p->dx_summed ? c.dx_splits * p->dx_tiles * tile_bytes : 0);
+  p->at_dw = take(c.dw_splits > 1 ? c.dw_splits * migemm::loss_tiles(c.products, width, H) * tile_bytes : 0);
   if (at > p->workspace_bytes) p->workspace_bytes = at;
 }
 
@@ -305,15 +306,15 @@ int gemm_vocab_loss_run(const migemm_vocab_loss_plan* p, const void* x, const vo
   s.V = d.vocab, s.H = d.hidden;
   s.parts = static_cast<float2*>(workspace);
   s.part_rows = p->chunk;
-  s.target_logit = reinterpret_cast<float*>(
-      s.parts + (d.vocab + migemm::kWaveTile - 1) / migemm::kWaveTile * p->chunk);
+  s.part_cols = migemm::kLossTileN[p->choice.forward] / 2;
+  s.target_logit = reinterpret_cast<float*>(s.parts + (d.vocab + s.part_cols - 1) / s.part_cols * p->chunk);
   for (int64_t r = 0; r < d.rows; r += p->chunk) {
     const int64_t rows = d.rows - r < p->chunk ? d.rows - r : p->chunk;
     s.gemm = product(rows, d.vocab, d.hidden, static_cast<const char*>(x) + r * d.x_rs * 2, d.x_rs,
                      true, w, d.w_rs, true, nullptr, 0);
     s.target = target + r, s.loss = loss + r, s.lse = lse + r;
-    const int grid = s.gemm.num_tiles < p->cus ? s.gemm.num_tiles : p->cus;
-    const hipError_t e = migemm::launch_loss_forward(s, grid, static_cast<hipStream_t>(stream));
+    const hipError_t e =
+        migemm::launch_loss_forward(s, p->choice.forward, p->cus, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return MIGEMM_ERR_LAUNCH;
   }
   return MIGEMM_OK;
@@ -338,41 +339,49 @@ int gemm_vocab_loss_run_backward(const migemm_vocab_loss_plan* p, const void* x,
   s.T = d.rows, s.V = d.vocab, s.H = d.hidden;
   s.x = x, s.x_rs = d.x_rs, s.dx = dx, s.dx_rs = d.dx_rs;
   s.target = target, s.lse = const_cast<float*>(lse), s.dloss = dloss;
-  s.count = reinterpret_cast<int*>(ws);
-  s.place = reinterpret_cast<int*>(ws + p->at_place);
+  s.head = reinterpret_cast<migemm::LossHead*>(ws);
   s.from = reinterpret_cast<int*>(ws + p->at_from);
   s.rows_lse = reinterpret_cast<float*>(ws + p->at_lse);
   s.rows_dloss = reinterpret_cast<float*>(ws + p->at_dloss);
   s.rows_target = reinterpret_cast<int*>(ws + p->at_target);
   s.rows_x = reinterpret_cast<unsigned short*>(ws + p->at_rows);
   s.rows_ld = p->rows_rs;
-  s.dx_sums = reinterpret_cast<migemm::dx_piece*>(ws + p->at_sums);
+  s.dx_sums = reinterpret_cast<migemm::mid_piece*>(ws + p->at_dx);
+  s.dw_sums = reinterpret_cast<migemm::mid_piece*>(ws + p->at_dw);
   s.dx_tiles = p->dx_tiles;
-  s.splits = p->splits;
+  s.splits = p->choice.dx_splits;
+  s.dw_splits = p->choice.dw_splits;
+  s.dx_summed = p->dx_summed;
   void* g = ws + p->at_g;
-  if (migemm::launch_loss_rows(s, hs) != hipSuccess) return MIGEMM_ERR_LAUNCH;
-  auto grid = [&](int64_t items) { return (int)(items < p->cus ? items : p->cus); };
-  for (int64_t c = 0; c < d.vocab; c += p->piece) {
+  hipError_t e = migemm::launch_loss_rows(s, hs);
+  for (int64_t c = 0; c < d.vocab && e == hipSuccess; c += p->piece) {
     const int64_t cols = d.vocab - c < p->piece ? d.vocab - c : p->piece;
     const char* wc = static_cast<const char*>(w) + c * d.w_rs * 2;
+    const bool last = c + cols == d.vocab;
     s.first_col = c;
     s.first_piece = c == 0;
     if (d.rows > 0) {
       s.gemm = product(d.rows, cols, d.hidden, s.rows_x, s.rows_ld, true, wc, d.w_rs, true, g, p->g_rs);
-      if (migemm::launch_loss_gradient(s, grid(s.gemm.num_tiles), hs) != hipSuccess)
-        return MIGEMM_ERR_LAUNCH;
+      e = migemm::launch_loss_gradient(s, p->choice.gradient, p->cus, hs);
+      if (e != hipSuccess) break;
     }
-    s.gemm = product(cols, d.hidden, d.rows, g, p->g_rs, false, s.rows_x, s.rows_ld, false,
-                     static_cast<char*>(dw) + c * d.dw_rs * 2, d.dw_rs);
-    if (migemm::launch_loss_dw(s, grid(s.gemm.num_tiles), hs) != hipSuccess) return MIGEMM_ERR_LAUNCH;
-    if (d.rows > 0) {
-      s.gemm = product(d.rows, d.hidden, cols, g, p->g_rs, true, wc, d.w_rs, false, nullptr, 0);
-      if (migemm::launch_loss_dx(s, grid(s.gemm.num_tiles * (int64_t)p->splits), hs) != hipSuccess)
-        return MIGEMM_ERR_LAUNCH;
+    const migemm::KernelArgs dw_of = product(cols, d.hidden, d.rows, g, p->g_rs, false, s.rows_x, s.rows_ld, false,
+                                             static_cast<char*>(dw) + c * d.dw_rs * 2, d.dw_rs);
+    const migemm::KernelArgs dx_of =
+        product(d.rows, d.hidden, cols, g, p->g_rs, true, wc, d.w_rs, false, dx, d.dx_rs);
+    s.gemm = dw_of;
+    if (p->choice.products != migemm::kLoss256) {
+      s.gemm_dx = dx_of;
+      e = migemm::launch_loss_products(s, p->choice.products, last, hs);
+      continue;
     }
+    e = migemm::launch_loss_dw(s, p->cus, hs);
+    if (e != hipSuccess || d.rows == 0) continue;
+    s.gemm = dx_of;
+    e = migemm::launch_loss_dx(s, p->cus, hs);
+    if (e == hipSuccess && last) e = migemm::launch_loss_dx_finish(s, hs);
   }
-  if (d.rows > 0 && migemm::launch_loss_dx_finish(s, hs) != hipSuccess) return MIGEMM_ERR_LAUNCH;
-  return MIGEMM_OK;
+  return launched(e);
 }
 
 int gemm_scaled_desc_validate(const migemm_scaled_desc* desc) { return validate_scaled(desc); }
