@@ -34,9 +34,10 @@ def _innermost_loops(lines):
     labels = {m.group(1): i for i, l in enumerate(lines) if (m := re.match(r"^(\.LBB\w+):", l))}
     loops = [(labels[m.group(1)], i) for i, l in enumerate(lines)
              if (m := re.search(r"s_c?branch\w*\s+(\.LBB\w+)", l)) and labels.get(m.group(1), i) < i]
+    loops = [(a, b) for a, b in loops if any("v_mfma" in x for x in lines[a:b])]
     inner = [(a, b) for a, b in loops
              if not any(a <= c and d <= b and (c, d) != (a, b) for c, d in loops)]
-    return [(a, b) for a, b in inner if any("v_mfma" in x for x in lines[a:b])]
+    return inner
 
 
 def test_no_scratch_access_inside_a_k_loop(kernels):

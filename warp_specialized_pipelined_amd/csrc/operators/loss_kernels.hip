@@ -30,8 +30,8 @@
 // for small ones launches and latency.
 #include <hip/hip_runtime.h>
 
-#include <stdio.h>
-#include <stdlib.h>
+#include <math.h>
+
 #include <type_traits>
 
 #include "../kernel/epilogue.hpp"
@@ -91,12 +91,17 @@ __device__ __forceinline__ void reduce_logits(f32x16 (&v)[BM][BN], const LossArg
 #pragma unroll
   for (int bi = 0; bi < BM; ++bi) {
     const int64_t row = m0 + 32 * bi + lr;
+    // (Block after block, and nothing shared between them: the accumulators
+    // leave few registers.)
+    sched_fence();
+    int first = 4 * half;  // the lane's columns are first + 32 bj + 8 q + c
+    asm volatile("" : "+v"(first));
     if (left < kCols) {
 #pragma unroll
       for (int bj = 0; bj < BN; ++bj)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) >= left) v[bi][bj][i] = -INFINITY;
+          v[bi][bj][i] = first + 32 * bj + 8 * (i >> 2) + (i & 3) < left ? v[bi][bj][i] : -INFINITY;
     }
     float m = v[bi][0][0];
 #pragma unroll
@@ -114,11 +119,13 @@ __device__ __forceinline__ void reduce_logits(f32x16 (&v)[BM][BN], const LossArg
     if (row < T && half == 0) part[row] = {m, sum};
     // (A row's target lies in one window of the vocabulary: the search is rare.)
     if (__ballot(want[bi] >= 0) != 0) {
+      const int at = want[bi] - 4 * half;  // of the lane's columns, 32 bj + 8 q + c
+      float found = 0.0f;
 #pragma unroll
       for (int bj = 0; bj < BN; ++bj)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) == want[bi]) s.target_logit[row] = v[bi][bj][i];
+        for (int i = 0; i < 16; ++i) found = 32 * bj + 8 * (i >> 2) + (i & 3) == at ? v[bi][bj][i] : found;
+      if (want[bi] >= 0 && (want[bi] & 4) == 4 * half) s.target_logit[row] = found;
     }
   }
 }
@@ -329,15 +336,23 @@ __device__ __forceinline__ void logits_to_gradient(f32x16 (&v)[BM][BN], const Lo
   }
 #pragma unroll
   for (int bi = 0; bi < BM; ++bi) {
-    const bool search = __ballot(want[bi] >= 0) != 0;
+    sched_fence();
 #pragma unroll
     for (int bj = 0; bj < BN; ++bj)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float p = exp_diff(v[bi][bj][i], lse[bi]);
-        if (search && 32 * bj + 8 * (i >> 2) + 4 * half + (i & 3) == want[bi]) p -= 1.0f;
-        v[bi][bj][i] = p * scale[bi];
-      }
+      for (int i = 0; i < 16; ++i) v[bi][bj][i] = exp_diff(v[bi][bj][i], lse[bi]);
+    // (A row's target lies in one window of the vocabulary: the search is rare.)
+    if (__ballot(want[bi] >= 0) != 0) {
+      const int at = want[bi] - 4 * half;  // of the lane's columns, 32 bj + 8 q + c
+#pragma unroll
+      for (int bj = 0; bj < BN; ++bj)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[bi][bj][i] -= 32 * bj + 8 * (i >> 2) + (i & 3) == at ? 1.0f : 0.0f;
+    }
+#pragma unroll
+    for (int bj = 0; bj < BN; ++bj)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[bi][bj][i] *= scale[bi];
   }
 }
 __device__ __forceinline__ f32x4 quarter_of(const f32x16& v, int q) {
@@ -419,7 +434,7 @@ __device__ __forceinline__ f32x4* dx_pieces(const LossArgs& s, int split, int64_
 // its own sums (the first piece of the vocabulary sets them).
 __global__ __launch_bounds__(kThreads, 1) void loss_dx_tiles(LossArgs s) {
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const KernelArgs a = with_rows(s, s.gemm);
+  const KernelArgs a = with_rows(s, s.gemm_dx);
   const int stages = (int)((a.K + 63) / 64);
   const int items = a.num_tiles * s.splits;
   Accum acc;
@@ -448,33 +463,12 @@ __global__ __launch_bounds__(kThreads, 1) void loss_dx_tiles(LossArgs s) {
   }
 }
 
-// dx of the rows that count: the splits' sums added in order, rounded once.
-// A workgroup takes 1/16 of a tile.
-__global__ __launch_bounds__(256) void loss_dx_finish(LossArgs s) {
-  const int64_t tile = blockIdx.x >> 4;
-  const int part = blockIdx.x & 15, wave = part >> 2, bi = part & 3;
-  const int tiles_n = s.gemm.tiles_n;
-  const int64_t tm = tile / tiles_n, tn = tile % tiles_n;
-  const int lane = threadIdx.x & 63, bj = threadIdx.x >> 6;
-  const int64_t row = tm * kTileM + (wave >> 1) * kWaveTile + 32 * bi + (lane & 31);
-  if (row >= s.head->count) return;
-  const float top = s.head->top;
-  unsigned short* d = static_cast<unsigned short*>(s.dx) + (int64_t)s.from[row] * s.dx_rs;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t c = tn * kTileN + (wave & 1) * kWaveTile + 32 * bj + 8 * q + 4 * (lane >> 5);
-    if (c >= s.H) continue;
-    f32x4 x = {0, 0, 0, 0};
-    for (int i = 0; i < s.splits; ++i) x += dx_pieces(s, i, tile, wave)[(4 * (4 * bi + bj) + q) * 64 + lane];
-    store4(d + c, s.H - c, x * top);
-  }
-}
-
-// The small tiles' two products, in one launch: workgroups 0 .. are the parts
-// of dx (K split dx_splits ways), those after them the parts of dw.  A product
+// The small tiles' products, in one launch if both take the same: the first
+// dx_items workgroups are the parts of dx (K split `splits` ways), those after
+// them the parts of dw.  A product
 // that one workgroup finishes is stored at once; else the sums go to memory in
 // register order (those of dx are added to from piece to piece) and
-// loss_finish_mid adds them up.
+// loss_finish adds them up.
 template <int TM, int TN, int SLOTS>
 __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_mid(LossArgs s) {
   typedef MidGeom<TM, TN, SLOTS> G;
@@ -482,7 +476,7 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
   const int count = s.head->count;
   const float top = s.head->top;
   const int dx_tiles_m = (int)((s.T + TM - 1) / TM), tiles_n = (int)((s.H + TN - 1) / TN);
-  const int dx_tiles = dx_tiles_m * tiles_n, dx_items = dx_tiles * s.splits;
+  const int dx_tiles = dx_tiles_m * tiles_n, dx_items = s.dx_items;
   const int slot = persistent_slot(blockIdx.x, gridDim.x);
   MidAccum<G::kBM, G::kBN> acc;
   if (slot < dx_items) {
@@ -532,7 +526,7 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
 // The sums of one 32 x 32 block of dx (the first dx_blocks workgroups) or dw,
 // added in the order of the splits, scaled and stored.
 template <int TM, int TN>
-__global__ __launch_bounds__(64) void loss_finish_mid(LossArgs s, int dx_blocks) {
+__global__ __launch_bounds__(64) void loss_finish(LossArgs s, int dx_blocks) {
   constexpr int BM = TM / 64, BN = TN / 64;
   const int lane = threadIdx.x;
   const bool dx = (int)blockIdx.x < dx_blocks;
@@ -541,7 +535,8 @@ __global__ __launch_bounds__(64) void loss_finish_mid(LossArgs s, int dx_blocks)
   const int tiles_m = (int)(((dx ? s.T : M) + TM - 1) / TM), tiles_n = (int)((s.H + TN - 1) / TN);
   const int part = at % (4 * BM * BN), tile = at / (4 * BM * BN);
   const int wave = part / (BM * BN), block = part % (BM * BN);
-  const MidTile t = mid_tile(tile, tiles_m, tiles_n);
+  // (loss_dx_tiles numbers its sums row by row of tiles.)
+  const MidTile t = TM == kTileM ? MidTile{tile / tiles_n, tile % tiles_n} : mid_tile(tile, tiles_m, tiles_n);
   const int64_t m = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM + 32 * (block / BN) + (lane & 31);
   const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN + 32 * (block % BN);
   if (m >= M || n0 >= s.H) return;
@@ -564,25 +559,98 @@ typedef void (*loss_fn)(LossArgs);
 struct MidKernels {
   int lds;
   loss_fn forward, gradient, products;
-  void (*finish)(LossArgs, int);
 };
 template <int TM, int TN, int SLOTS>
 constexpr MidKernels mid_kernels() {
   return {(int)MidGeom<TM, TN, SLOTS>::kLds, loss_forward_mid<TM, TN, SLOTS>, loss_gradient_mid<TM, TN, SLOTS>,
-          loss_products_mid<TM, TN, SLOTS>, loss_finish_mid<TM, TN>};
+          loss_products_mid<TM, TN, SLOTS>};
 }
-const MidKernels kMid[] = {mid_kernels<128, 128, 4>(), mid_kernels<64, 64, 4>(), mid_kernels<64, 128, 3>(), mid_kernels<128, 128, 2>()};  // from kLoss128 on
+// From kLoss128 on.
+const MidKernels kMid[] = {mid_kernels<128, 128, 2>(), mid_kernels<64, 128, 3>(), mid_kernels<64, 64, 4>()};
+void (*const kFinish[])(LossArgs, int) = {loss_finish<256, 256>, loss_finish<128, 128>, loss_finish<64, 128>,
+                                          loss_finish<64, 64>};
+
+// What the tiles cost, in microseconds: a K stage of 64 with one tile a
+// compute unit and with two, and a tile besides, by what it makes.
+enum LossProduct { kForward, kGradient, kDw, kDx };
+struct LossCost {
+  int per_cu;
+  double stage1, stage2, tile[4];
+};
+const LossCost kCost[kLossTiles] = {{1, 1.26, 1.26, {14.6, 14.6, 10.7, 7.2}},
+                                    {2, 0.66, 1.00, {3.1, 4.6, 2.8, 3.2}},
+                                    {2, 0.42, 0.69, {2.5, 4.1, 2.5, 2.7}},
+                                    {2, 0.35, 0.50, {2.3, 3.2, 1.7, 2.1}}};
+// Microseconds for a rows x cols product of `bytes` in all, its K of `stages`
+// stages split; and the workgroups that takes.
+struct ProductCost {
+  double us, items;
+};
+ProductCost cost_of(int tile, LossProduct what, int64_t rows, int64_t cols, int64_t stages, int splits, double bytes,
+                    int cu_count) {
+  const LossCost& c = kCost[tile];
+  const double items = (double)loss_tiles(tile, rows, cols) * splits, st = ceil((double)stages / splits);
+  const double at_once = (double)c.per_cu * cu_count, full = floor(items / at_once), rest = items - full * at_once;
+  double t = full * (st * c.stage2 + c.tile[what]);
+  if (rest > 0) t += st * (rest <= cu_count ? c.stage1 : c.stage2) + c.tile[what];
+  const double memory = bytes / 5.1e6;
+  return {2.5 + (t > memory ? t : memory), items};
+}
 
 }  // namespace
 
+// The tiles and splits that cost least.  The figures are a fit to 140 losses
+// of 1 to 8192 rows, 100 to 131072 entries and hidden sizes of 64 to 4096, each
+// product timed in every tile and with up to five splits; what it picks is 2 to
+// 4% slower than the fastest of them on average.
 LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_count) {
-  LossChoice c = {0, 0, 0, 1, 1};
-  const int64_t stages = ((piece < V ? piece : V) + 63) / 64, dx_tiles = loss_tiles(kLoss256, T, H);
-  int64_t splits = dx_tiles > 0 ? cu_count / dx_tiles : 1;
-  splits = splits > stages / 8 ? stages / 8 : splits;
-  c.dx_splits = splits < 1 ? 1 : (int)splits;
-  if (const char* e = getenv("MIGEMM_L"))
-    sscanf(e, "%d,%d,%d,%d,%d", &c.forward, &c.gradient, &c.products, &c.dx_splits, &c.dw_splits);
+  LossChoice c = {};
+  const int64_t W = piece < V ? piece : V, sh = (H + 63) / 64, sw = (W + 63) / 64, st = (T + 63) / 64;
+  const double t = (double)T, v = (double)V, h = (double)H, w = (double)W;
+  double least_f = 1e300, least_g = 1e300;
+  for (int i = 0; i < kLossTiles; ++i) {
+    // (A row's pairs, one for half a tile's columns, are written and joined.)
+    const double f = cost_of(i, kForward, T, V, sh, 1, 2 * h * (t + v), cu_count).us +
+                     16 * t * (v / (kLossTileN[i] / 2)) / 4e6;
+    if (f < least_f) least_f = f, c.forward = i;
+    const double g = cost_of(i, kGradient, T, W, sh, 1, 2 * (h * (t + w) + t * w), cu_count).us;
+    if (g < least_g) least_g = g, c.gradient = i;
+  }
+  // Both products' tiles and splits together: alike, they share the launches.
+  double least = 1e300;
+  constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+  const double launch = 3.5;
+  auto finish = [&](int splits, double elements) {
+    return launch + 0.15 * splits + (4.0 * splits + 2) * elements / 4.5e6;
+  };
+  for (int x = 0; x < kLossTiles; ++x)
+    for (int xs : kSplits) {
+      const bool summed = x == kLoss256 || xs > 1 || W < V;
+      const double sums = 4 * t * h * xs;
+      if (xs > 1 && (sw < 3 * xs || sums > (512 << 20))) break;
+      const ProductCost dx =
+          cost_of(x, kDx, T, H, sw, xs, 2 * (t * w + w * h) + (summed ? sums : 2 * t * h), cu_count);
+      const double dx_end = summed ? finish(xs, t * h) : 0;
+      for (int y = 0; y < kLossTiles; ++y)
+        for (int ys : kSplits) {
+          if (ys > 1 && (y == kLoss256 || st < 3 * ys || 4 * w * h * ys > (512 << 20))) break;
+          const ProductCost dw =
+              cost_of(y, kDw, W, H, st, ys, 2 * (t * w + t * h) + (ys > 1 ? 4 * ys : 2) * w * h, cu_count);
+          const double dw_end = ys > 1 ? finish(ys, w * h) : 0;
+          double both = dx.us + dw.us + launch + dx_end + dw_end;
+          if (x == y && x != kLoss256) {
+            // Side by side where both fit the chip.
+            both = dx.items + dw.items <= kCost[x].per_cu * (double)cu_count
+                       ? (dx.us > dw.us ? dx.us : dw.us) + 1
+                       : dx.us + dw.us - 2.5;
+            both += dx_end + dw_end - (dx_end > 0 && dw_end > 0 ? launch : 0);
+          }
+          if (both < least) {
+            least = both;
+            c.dx = x, c.dx_splits = xs, c.dw = y, c.dw_splits = ys;
+          }
+        }
+    }
   return c;
 }
 
@@ -639,28 +707,40 @@ hipError_t launch_loss_gradient(const LossArgs& s, int tile, int cu_count, hipSt
   }
   return hipSuccess;
 }
-hipError_t launch_loss_dw(const LossArgs& s, int cu_count, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_dw_tiles, s.gemm.num_tiles < cu_count ? s.gemm.num_tiles : cu_count, kThreads,
-                kPlainLdsBytes, s);
-  return hipSuccess;
-}
-hipError_t launch_loss_dx(const LossArgs& s, int cu_count, hipStream_t stream) {
-  const int64_t items = (int64_t)s.gemm.num_tiles * s.splits;
-  MIGEMM_LAUNCH(loss_dx_tiles, items < cu_count ? items : cu_count, kThreads, kPlainLdsBytes, s);
-  return hipSuccess;
-}
-hipError_t launch_loss_dx_finish(const LossArgs& s, hipStream_t stream) {
-  MIGEMM_LAUNCH(loss_dx_finish, s.dx_tiles * 16, 256, 0, s);
-  return hipSuccess;
-}
-hipError_t launch_loss_products(const LossArgs& s, int tile, bool last_piece, hipStream_t stream) {
-  const int blocks = (kLossTileM[tile] / 32) * (kLossTileN[tile] / 32);
-  const MidKernels& m = kMid[tile - 1];
-  const int64_t dw_tiles = loss_tiles(tile, s.gemm.M, s.H);
-  MIGEMM_LAUNCH(m.products, s.dx_tiles * s.splits + dw_tiles * s.dw_splits, 256, m.lds, s);
-  const int64_t dx_blocks = s.dx_summed && last_piece ? s.dx_tiles * blocks : 0;
-  const int64_t dw_blocks = s.dw_splits > 1 ? dw_tiles * blocks : 0;
-  if (dx_blocks + dw_blocks > 0) MIGEMM_LAUNCH(m.finish, dx_blocks + dw_blocks, 64, 0, s, (int)dx_blocks);
+hipError_t launch_loss_products(const LossArgs& args, const LossChoice& c, bool last_piece, int cu_count,
+                                hipStream_t stream) {
+  LossArgs s = args;
+  const int64_t dx_items = s.dx_tiles * s.splits;
+  const int64_t dw_tiles = loss_tiles(c.dw, s.gemm.M, s.H), dw_items = dw_tiles * s.dw_splits;
+  auto blocks = [](int tile) { return (kLossTileM[tile] / 32) * (kLossTileN[tile] / 32); };
+  const int64_t dx_blocks = s.dx_summed && last_piece ? s.dx_tiles * blocks(c.dx) : 0;
+  const int64_t dw_blocks = s.dw_splits > 1 ? dw_tiles * blocks(c.dw) : 0;
+  const bool together = c.dx == c.dw && c.dx != kLoss256;
+  if (together) {
+    s.dx_items = (int)dx_items;
+    MIGEMM_LAUNCH(kMid[c.dx - 1].products, dx_items + dw_items, 256, kMid[c.dx - 1].lds, s);
+  } else {
+    if (c.dw == kLoss256) {
+      MIGEMM_LAUNCH(loss_dw_tiles, dw_items < cu_count ? dw_items : cu_count, kThreads, kPlainLdsBytes, s);
+    } else {
+      s.dx_items = 0;
+      MIGEMM_LAUNCH(kMid[c.dw - 1].products, dw_items, 256, kMid[c.dw - 1].lds, s);
+    }
+    if (dx_items > 0) {
+      if (c.dx == kLoss256) {
+        MIGEMM_LAUNCH(loss_dx_tiles, dx_items < cu_count ? dx_items : cu_count, kThreads, kPlainLdsBytes, s);
+      } else {
+        s.dx_items = (int)dx_items;
+        MIGEMM_LAUNCH(kMid[c.dx - 1].products, dx_items, 256, kMid[c.dx - 1].lds, s);
+      }
+    }
+  }
+  if (together && dx_blocks + dw_blocks > 0) {
+    MIGEMM_LAUNCH(kFinish[c.dx], dx_blocks + dw_blocks, 64, 0, s, (int)dx_blocks);
+    return hipSuccess;
+  }
+  if (dw_blocks > 0) MIGEMM_LAUNCH(kFinish[c.dw], dw_blocks, 64, 0, s, 0);
+  if (dx_blocks > 0) MIGEMM_LAUNCH(kFinish[c.dx], dx_blocks, 64, 0, s, (int)dx_blocks);
   return hipSuccess;
 }
 

@@ -7,10 +7,16 @@
 // each operand row, loaded straight into LDS.  What differs is that a small
 // tile's stage is worth only 128 or 512 cycles of matrix instructions, less
 // than a load takes to arrive and little more than an LDS read and a barrier
-// do.  So the ring has SLOTS stages, all of them in flight or waiting while
-// one more, the stage being multiplied, is wholly in registers: an iteration
-// reads stage d + 1's fragments and issues stage d + SLOTS's loads under the
-// products of stage d, and meets one barrier.
+// do.  Two schedules:
+//   SLOTS > 2, for few tiles with much K: the ring has SLOTS stages, all of
+//     them in flight or waiting while one more, the stage being multiplied, is
+//     wholly in registers: an iteration reads stage d + 1's fragments and
+//     issues stage d + SLOTS's loads under the products of stage d, and meets
+//     one barrier.
+//   SLOTS = 2, for many tiles with little K: fragments one k-step ahead, as
+//     in the 256 x 256 loop, in half the registers and half the LDS, so that
+//     two 128 x 128 workgroups share a compute unit and one's loads arrive
+//     under the other's products, prologue and epilogue.
 //
 // Bound: the loads.  A compute unit's L1 takes 31 cycles for 1 KiB of them
 // (17 of address work, 14 stalled on lines on their way; counters over
@@ -213,15 +219,36 @@ __device__ __forceinline__ void mid_loop(MidAccum<TM / 64, TN / 64>& acc, const 
 #pragma unroll
     for (int j = 0; j < BN; ++j) acc.v[i][j] = f32x16{};
 
-  // Two stages' fragments: the one being multiplied, the one being read.
-  frag_t fa[2][KS][BM], fb[2][KS][BN];
-  constexpr int kReads = KS * (BM + BN), kProducts = KS * BM * BN;
-  // Fragment x of a stage, k-step by k-step: A's BM blocks, then B's BN.
-  auto read = [&](auto bc, auto xc, uint32_t slot) {
-    constexpr int b = decltype(bc)::value, ks = decltype(xc)::value / (BM + BN);
-    constexpr int x = decltype(xc)::value % (BM + BN);
-    if constexpr (x < BM) fa[b][ks][x] = ra.template read<x, ks>(slot);
-    else fb[b][ks][x - BM] = rb.template read<x - BM, ks>(slot + T::kPartA);
+  // Fragments: of two stages (the one being multiplied, the one being read),
+  // or with two slots of two k-steps.
+  constexpr bool kDeep = SLOTS > 2;
+  constexpr int FS = kDeep ? KS : 1;
+  frag_t fa[2][FS][BM], fb[2][FS][BN];
+  constexpr int P = BM * BN, R = BM + BN;
+  // Fragment x of k-step KSTEP (A's BM blocks, then B's BN) into buffer b, place f.
+  auto read = [&](auto bc, auto fc, auto kc, auto xc, uint32_t slot) {
+    constexpr int b = decltype(bc)::value, f = decltype(fc)::value, ks = decltype(kc)::value;
+    constexpr int x = decltype(xc)::value;
+    if constexpr (x < BM) fa[b][f][x] = ra.template read<x, ks>(slot);
+    else fb[b][f][x - BM] = rb.template read<x - BM, ks>(slot + T::kPartA);
+  };
+  // Product m of the k-step in buffer b, place f.
+  WideFrag wa[EXACT ? BM : 1], wb[EXACT ? BN : 1];
+  auto multiply = [&](auto bc, auto fc, auto mc) {
+    constexpr int b = decltype(bc)::value, f = decltype(fc)::value;
+    constexpr int i = decltype(mc)::value / BN, j = decltype(mc)::value % BN;
+    if constexpr (EXACT) {
+      if constexpr (i == 0 && j == 0) {
+#pragma unroll
+        for (int x = 0; x < BM; ++x) wa[x] = widen_frag(fa[b][f][x]);
+#pragma unroll
+        for (int x = 0; x < BN; ++x) wb[x] = widen_frag(fb[b][f][x]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc.v[i][j] = mfma<2>(wb[j].v[q], wa[i].v[q], acc.v[i][j]);
+    } else {
+      acc.v[i][j] = mfma<ES>(fb[b][f][j], fa[b][f][i], acc.v[i][j]);
+    }
   };
   // Load j of a stage: A's, then B's.
   auto load = [&](const auto& sa, const auto& sb, auto jc, uint32_t slot) {
@@ -240,74 +267,117 @@ __device__ __forceinline__ void mid_loop(MidAccum<TM / 64, TN / 64>& acc, const 
       }
     }
   };
-  auto after = [](uint32_t slot) { return slot + T::kSlot == T::kRing ? 0 : slot + T::kSlot; };
-
-  // Stage d from buffer b; stage d + 1 (in slot `nxt`) into the other buffer;
-  // stage d + SLOTS loaded into `cur`, which stage d's reads left free.  The
-  // reads go first, one or two in front of each product, and the loads one
-  // behind each product from the first on (the address path takes 16 cycles
-  // a load and four waves share it: in a burst they stall what follows).
-  uint32_t cur = 0;
-  auto stage = [&](auto bc, int d) {
-    constexpr int b = decltype(bc)::value;
-    const uint32_t nxt = after(cur);
-    const auto sa = la.next();
-    const auto sb = lb.next();
-    static_for<0, KS>([&](auto kc) {
-      constexpr int ks = decltype(kc)::value;
-      WideFrag wa[EXACT ? BM : 1], wb[EXACT ? BN : 1];
-      if constexpr (EXACT) {
-#pragma unroll
-        for (int i = 0; i < BM; ++i) wa[i] = widen_frag(fa[b][ks][i]);
-#pragma unroll
-        for (int j = 0; j < BN; ++j) wb[j] = widen_frag(fb[b][ks][j]);
-      }
-      static_for<0, BM * BN>([&](auto mc) {
-        constexpr int m = decltype(mc)::value, i = m / BN, j = m % BN, at = ks * BM * BN + m;
-        sched_fence();
-        static_for<at * kReads / kProducts, (at + 1) * kReads / kProducts>(
-            [&](auto xc) { read(std::integral_constant<int, 1 - b>{}, xc, nxt); });
-        if constexpr (EXACT) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc.v[i][j] = mfma<2>(wb[j].v[q], wa[i].v[q], acc.v[i][j]);
-        } else {
-          acc.v[i][j] = mfma<ES>(fb[b][ks][j], fa[b][ks][i], acc.v[i][j]);
-        }
-        static_for<at * kLoads / kProducts, (at + 1) * kLoads / kProducts>(
-            [&](auto jc) { load(sa, sb, jc, cur); });
-      });
-    });
-    // This wave's part of stage d + 2 has landed and its reads of stage d + 1
-    // have returned; past the barrier that holds for every wave.
+  // Waits until all but the last `ahead` (at most SLOTS - 1) stages' loads have landed.
+  auto landed = [&](int ahead) {
     sched_fence();
-    wait_vmcnt<kLoads*(SLOTS - 2)>();
-    wait_lgkmcnt<0>();
-    clear_tail(d + 2, after(nxt));
-    barrier();
-    cur = nxt;
+    static_for<0, SLOTS>([&](auto ac) {
+      constexpr int n = decltype(ac)::value;
+      if (ahead == n) wait_vmcnt<kLoads * n>();
+    });
+    sched_fence();
   };
-  if (KT > 0) {
-    // (Stages past the last one only zero a free slot: the count of loads in
-    // flight is then the same in every iteration.)
-    static_for<0, SLOTS>([&](auto sc) {
+  auto after = [](uint32_t slot) { return slot + T::kSlot == T::kRing ? 0 : slot + T::kSlot; };
+  const std::integral_constant<int, 0> zero;
+
+  static_for<0, SLOTS>([&](auto sc) {
+    if (decltype(sc)::value < KT) {
       const auto sa = la.next();
       const auto sb = lb.next();
       static_for<0, kLoads>([&](auto jc) { load(sa, sb, jc, decltype(sc)::value * T::kSlot); });
-    });
-    wait_vmcnt<kLoads*(SLOTS - 1)>();
+    }
+  });
+  if (KT > 0) {
+    landed(KT - 1 < SLOTS - 1 ? KT - 1 : SLOTS - 1);
     clear_tail(0, 0);
     barrier();
-    static_for<0, kReads>([&](auto xc) { read(std::integral_constant<int, 0>{}, xc, 0); });
-    sched_fence();
-    wait_vmcnt<kLoads*(SLOTS - 2)>();
-    wait_lgkmcnt<0>();
-    clear_tail(1, T::kSlot);
-    barrier();
   }
-  for (int d = 0; d < KT; d += 2) {
-    stage(std::integral_constant<int, 0>{}, d);
-    if (d + 1 == KT) break;
-    stage(std::integral_constant<int, 1>{}, d + 1);
+  uint32_t cur = 0;
+  if constexpr (kDeep) {
+    // Stage d from buffer b; stage d + 1 (in slot `nxt`) into the other buffer;
+    // stage d + SLOTS loaded into `cur`, which stage d's reads left free.  The
+    // reads go first, one or two in front of each product, and the loads one
+    // behind each product from the first on (the address path takes 16 cycles
+    // a load and four waves share it: in a burst they stall what follows).
+    auto stage = [&](auto bc, int d) {
+      constexpr int b = decltype(bc)::value;
+      const uint32_t nxt = after(cur);
+      const bool more = d + SLOTS < KT;
+      const auto sa = la.next();
+      const auto sb = lb.next();
+      static_for<0, KS * P>([&](auto mc) {
+        constexpr int m = decltype(mc)::value;
+        sched_fence();
+        static_for<m * KS * R / (KS * P), (m + 1) * KS * R / (KS * P)>([&](auto xc) {
+          constexpr int x = decltype(xc)::value;
+          read(std::integral_constant<int, 1 - b>{}, std::integral_constant<int, x / R>{},
+               std::integral_constant<int, x / R>{}, std::integral_constant<int, x % R>{}, nxt);
+        });
+        multiply(bc, std::integral_constant<int, m / P>{}, std::integral_constant<int, m % P>{});
+        static_for<m * kLoads / (KS * P), (m + 1) * kLoads / (KS * P)>([&](auto jc) {
+          if (more) load(sa, sb, jc, cur);
+        });
+      });
+      // This wave's part of stage d + 2 has landed and its reads of stage d + 1
+      // have returned; past the barrier that holds for every wave.
+      const int ahead = KT - 3 - d;
+      landed(ahead < 0 ? 0 : (ahead < SLOTS - 2 ? ahead : SLOTS - 2));
+      wait_lgkmcnt<0>();
+      clear_tail(d + 2, after(nxt));
+      barrier();
+      cur = nxt;
+    };
+    if (KT > 0) {
+      static_for<0, KS * R>([&](auto xc) {
+        constexpr int x = decltype(xc)::value;
+        read(zero, std::integral_constant<int, x / R>{}, std::integral_constant<int, x / R>{},
+             std::integral_constant<int, x % R>{}, 0);
+      });
+      landed(KT < 2 ? 0 : (KT - 2 < SLOTS - 2 ? KT - 2 : SLOTS - 2));
+      wait_lgkmcnt<0>();
+      clear_tail(1, T::kSlot);
+      barrier();
+    }
+    for (int d = 0; d < KT; d += 2) {
+      stage(std::integral_constant<int, 0>{}, d);
+      if (d + 1 == KT) break;
+      stage(std::integral_constant<int, 1>{}, d + 1);
+    }
+  } else {
+    if (KT > 0) static_for<0, R>([&](auto xc) { read(zero, zero, zero, xc, 0); });
+    for (int d = 0; d < KT; ++d) {
+      const uint32_t nxt = after(cur);
+      static_for<0, KS - 1>([&](auto kc) {
+        constexpr int ks = decltype(kc)::value;
+        static_for<0, P>([&](auto mc) {
+          constexpr int m = decltype(mc)::value;
+          sched_fence();
+          static_for<m * R / P, (m + 1) * R / P>([&](auto xc) {
+            read(std::integral_constant<int, (ks + 1) & 1>{}, zero, std::integral_constant<int, ks + 1>{}, xc, cur);
+          });
+          multiply(std::integral_constant<int, ks & 1>{}, zero, mc);
+        });
+      });
+      // Stage d + 1 has landed and this wave's reads of stage d have returned;
+      // past the barrier that holds for every wave, and stage d + 2 may be
+      // loaded over stage d.
+      landed(0);
+      wait_lgkmcnt<0>();
+      clear_tail(d + 1, nxt);
+      barrier();
+      const bool more = d + 2 < KT;
+      const auto sa = la.next();
+      const auto sb = lb.next();
+      static_for<0, P>([&](auto mc) {
+        constexpr int m = decltype(mc)::value;
+        sched_fence();
+        static_for<m * R / P, (m + 1) * R / P>([&](auto xc) { read(zero, zero, zero, xc, nxt); });
+        multiply(std::integral_constant<int, (KS - 1) & 1>{}, zero, mc);
+        static_for<m * kLoads / P, (m + 1) * kLoads / P>([&](auto jc) {
+          if (more) load(sa, sb, jc, cur);
+        });
+      });
+      cur = nxt;
+    }
   }
   sched_fence();
   wait_vmcnt<0>();

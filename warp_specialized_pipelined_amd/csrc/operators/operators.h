@@ -106,14 +106,15 @@ struct LossArgs {
   mid_piece* dw_sums;     // [dw_splits][tiles of dw]
   int64_t dx_tiles;
   int32_t splits, dw_splits;
+  int32_t dx_items;       // loss_products_mid: its workgroups that form dx
   int32_t first_piece, dx_summed;
 };
 
 // Tiles of the loss's products: 256 x 256 (the GEMM's K loop) or smaller
 // (midtile.hpp).
-enum LossTile { kLoss256, kLoss128, kLoss64, kLoss64x128, kLoss128b };
-constexpr int kLossTileM[] = {256, 128, 64, 64, 128};
-constexpr int kLossTileN[] = {256, 128, 64, 128, 128};
+enum LossTile { kLoss256, kLoss128, kLoss64x128, kLoss64, kLossTiles };
+constexpr int kLossTileM[] = {256, 128, 64, 64};
+constexpr int kLossTileN[] = {256, 128, 128, 64};
 inline int64_t loss_tiles(int tile, int64_t rows, int64_t cols) {
   return ((rows + kLossTileM[tile] - 1) / kLossTileM[tile]) * ((cols + kLossTileN[tile] - 1) / kLossTileN[tile]);
 }
@@ -122,7 +123,7 @@ inline int64_t loss_tiles(int tile, int64_t rows, int64_t cols) {
 // products, and the ways K of those is split.  `piece`: vocabulary entries
 // that the backward pass takes at a time.
 struct LossChoice {
-  int forward, gradient, products, dx_splits, dw_splits;
+  int forward, gradient, dx, dw, dx_splits, dw_splits;
 };
 LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_count);
 
@@ -130,11 +131,9 @@ hipError_t prepare_loss();
 hipError_t launch_loss_forward(const LossArgs& s, int tile, int cu_count, hipStream_t stream);
 hipError_t launch_loss_rows(const LossArgs& s, hipStream_t stream);
 hipError_t launch_loss_gradient(const LossArgs& s, int tile, int cu_count, hipStream_t stream);
-// 256 x 256 tiles: dw, dx, and after the last piece what dx's sums come to.
-hipError_t launch_loss_dw(const LossArgs& s, int cu_count, hipStream_t stream);
-hipError_t launch_loss_dx(const LossArgs& s, int cu_count, hipStream_t stream);
-hipError_t launch_loss_dx_finish(const LossArgs& s, hipStream_t stream);
-// Smaller tiles: both, and what is summed of them.
-hipError_t launch_loss_products(const LossArgs& s, int tile, bool last_piece, hipStream_t stream);
+// dw of a piece (s.gemm) and its share of dx (s.gemm_dx; after the last piece
+// dx itself).
+hipError_t launch_loss_products(const LossArgs& s, const LossChoice& c, bool last_piece, int cu_count,
+                                hipStream_t stream);
 
 }  // namespace migemm

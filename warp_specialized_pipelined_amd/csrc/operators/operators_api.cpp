@@ -230,9 +230,9 @@ void lay_out_loss(migemm_vocab_loss_plan* p) {
   const int64_t width = p->piece < V ? p->piece : V;
   p->g_rs = up(width, 64) + 64;  // rows not a power of two apart
   p->rows_rs = up(H, 64);
-  const int64_t tile_bytes = 4 * migemm::kLossTileM[c.products] * migemm::kLossTileN[c.products];
-  p->dx_tiles = migemm::loss_tiles(c.products, T, H);
-  p->dx_summed = c.products == migemm::kLoss256 || c.dx_splits > 1 || p->piece < V;
+  auto tile_bytes = [](int tile) { return (int64_t)4 * migemm::kLossTileM[tile] * migemm::kLossTileN[tile]; };
+  p->dx_tiles = migemm::loss_tiles(c.dx, T, H);
+  p->dx_summed = c.dx == migemm::kLoss256 || c.dx_splits > 1 || p->piece < V;
   size_t at = 256;  // the head
   auto take = [&](int64_t bytes) {
     const size_t from = at;
@@ -245,8 +245,8 @@ void lay_out_loss(migemm_vocab_loss_plan* p) {
   p->at_target = take(T * 4);
   p->at_rows = take(T * p->rows_rs * 2);
   p->at_g = take(T * p->g_rs * 2);
-  p->at_dx = take(p->dx_summed ? c.dx_splits * p->dx_tiles * tile_bytes : 0);
-  p->at_dw = take(c.dw_splits > 1 ? c.dw_splits * migemm::loss_tiles(c.products, width, H) * tile_bytes : 0);
+  p->at_dx = take(p->dx_summed ? c.dx_splits * p->dx_tiles * tile_bytes(c.dx) : 0);
+  p->at_dw = take(c.dw_splits > 1 ? c.dw_splits * migemm::loss_tiles(c.dw, width, H) * tile_bytes(c.dw) : 0);
   if (at > p->workspace_bytes) p->workspace_bytes = at;
 }
 
@@ -365,21 +365,10 @@ int gemm_vocab_loss_run_backward(const migemm_vocab_loss_plan* p, const void* x,
       e = migemm::launch_loss_gradient(s, p->choice.gradient, p->cus, hs);
       if (e != hipSuccess) break;
     }
-    const migemm::KernelArgs dw_of = product(cols, d.hidden, d.rows, g, p->g_rs, false, s.rows_x, s.rows_ld, false,
-                                             static_cast<char*>(dw) + c * d.dw_rs * 2, d.dw_rs);
-    const migemm::KernelArgs dx_of =
-        product(d.rows, d.hidden, cols, g, p->g_rs, true, wc, d.w_rs, false, dx, d.dx_rs);
-    s.gemm = dw_of;
-    if (p->choice.products != migemm::kLoss256) {
-      s.gemm_dx = dx_of;
-      e = migemm::launch_loss_products(s, p->choice.products, last, hs);
-      continue;
-    }
-    e = migemm::launch_loss_dw(s, p->cus, hs);
-    if (e != hipSuccess || d.rows == 0) continue;
-    s.gemm = dx_of;
-    e = migemm::launch_loss_dx(s, p->cus, hs);
-    if (e == hipSuccess && last) e = migemm::launch_loss_dx_finish(s, hs);
+    s.gemm = product(cols, d.hidden, d.rows, g, p->g_rs, false, s.rows_x, s.rows_ld, false,
+                     static_cast<char*>(dw) + c * d.dw_rs * 2, d.dw_rs);
+    s.gemm_dx = product(d.rows, d.hidden, cols, g, p->g_rs, true, wc, d.w_rs, false, dx, d.dx_rs);
+    e = migemm::launch_loss_products(s, p->choice, last, p->cus, hs);
   }
   return launched(e);
 }
