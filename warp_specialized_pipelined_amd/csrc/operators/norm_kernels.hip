@@ -203,14 +203,16 @@ __global__ __launch_bounds__(threads_of(WAVES)) void norm_forward(NormArgs a) {
 
 // Each walker (a workgroup, or with WAVES = 1 a wave) takes rows walker,
 // walker + walkers, ... and keeps its columns' sums of g n in registers; the
-// sums go to the walker's row of the workspace, and norm_sum_partials adds
-// those rows in a fixed order: no atomics, the same result on every run.
+// workgroup's sums (with WAVES = 1 its four waves', added through LDS) go to
+// its row of the workspace, and norm_sum_partials adds those rows in a fixed
+// order: no atomics, the same result on every run.  One workgroup alone writes
+// dweight itself.
 template <int WAVES, int NV, bool RES>
 __global__ __launch_bounds__(threads_of(WAVES)) void norm_backward(NormArgs a) {
   constexpr int kLanes = 64 * WAVES;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t walker = (int64_t)blockIdx.x * rows_of(WAVES) + (WAVES == 1 ? wave : 0);
-  if (walker >= a.partial_rows) return;
+  const int64_t walkers = (int64_t)gridDim.x * rows_of(WAVES);
   const int t = WAVES == 1 ? lane : (int)threadIdx.x;
   const unsigned short* w = static_cast<const unsigned short*>(a.weight);
   const float cols = (float)a.cols;
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(threads_of(WAVES)) void norm_backward(NormArgs a) {
   }
   __shared__ float sums[2][WAVES];
   int phase = 0;
-  for (int64_t row = walker; row < a.rows; row += a.partial_rows) {
+  for (int64_t row = walker; row < a.rows; row += walkers) {
     const unsigned short* g = static_cast<const unsigned short*>(a.dy) + row * a.dy_rs;
     const unsigned short* h = static_cast<const unsigned short*>(a.x) + row * a.x_rs;
     u32x4 gv[NV], hv[NV], dhv[NV];
@@ -280,33 +282,52 @@ __global__ __launch_bounds__(threads_of(WAVES)) void norm_backward(NormArgs a) {
       store8(dx, (int64_t)(i * kLanes + t) * 8, a.cols, o);
     }
   }
-  float* p = a.partials + walker * a.cols;
+  float* p = a.partial_rows == 1 ? a.dweight : a.partials + (int64_t)blockIdx.x * a.cols;
+  if constexpr (WAVES == 1) {
+    __shared__ float all[4][NV * 512];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t)(i * kLanes + t) * 8;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < a.cols) p[c + e] = dw[i][e];
+      for (int e = 0; e < 8; ++e) all[wave][(i * 64 + lane) * 8 + e] = dw[i][e];
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < a.cols; c += 256) p[c] = ((all[0][c] + all[1][c]) + all[2][c]) + all[3][c];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * kLanes + t) * 8;
+      if (c + 8 <= a.cols) {
+        // (16-byte stores, which need an address that is a multiple of 4.)
+        typedef float f32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+        *reinterpret_cast<f32x4_4*>(p + c) = f32x4_4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        *reinterpret_cast<f32x4_4*>(p + c + 4) = f32x4_4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < a.cols) p[c + e] = dw[i][e];
+      }
+    }
   }
 }
 
-// dweight[c] = sum over partial rows, 32 columns a workgroup: 32 threads a
-// column add every 32nd row, then one adds the 32 sums in order.
-__global__ __launch_bounds__(1024) void norm_sum_partials(NormArgs a) {
-  __shared__ float part[32][33];
-  const int col = threadIdx.x & 31, group = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+// dweight[c] = sum over partial rows: GROUPS threads a column add every
+// GROUPS-th row, then one adds their sums in order.
+template <int GROUPS, int COLS>
+__global__ __launch_bounds__(GROUPS * COLS) void norm_sum_partials(NormArgs a) {
+  const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
+  const int64_t c = (int64_t)blockIdx.x * COLS + col;
   float s = 0.0f;
   if (c < a.cols)
-    for (int64_t p = group; p < a.partial_rows; p += 32) s += a.partials[p * a.cols + c];
-  part[group][col] = s;
-  __syncthreads();
-  if (group == 0 && c < a.cols) {
-    s = 0.0f;
+#pragma unroll 8
+    for (int64_t p = group; p < a.partial_rows; p += GROUPS) s += a.partials[p * a.cols + c];
+  if constexpr (GROUPS > 1) {
+    __shared__ float part[GROUPS][COLS + 1];
+    part[group][col] = s;
+    __syncthreads();
+    if (group != 0) return;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += part[i][col];
-    a.dweight[c] = s;
+    for (int i = 1; i < GROUPS; ++i) s += part[i][col];
   }
+  if (c < a.cols) a.dweight[c] = s;
 }
 
 typedef void (*norm_fn)(NormArgs);
@@ -329,9 +350,10 @@ norm_fn backward_pick(int nv, bool res) {
                  : (nv == 2 ? norm_backward<WAVES, 2, false> : norm_backward<WAVES, 4, false>);
 }
 
-// The fewest waves from `waves` on (1, 4, 16) whose lanes hold the row in
-// `most` vectors, and the vectors that takes.
-NormShape shape_for(int64_t cols, int waves, int most) {
+// The fewest waves (1, 4, 16) whose lanes hold the row in `most` vectors, and
+// the vectors that takes.
+NormShape shape_for(int64_t cols, int most) {
+  int waves = 1;
   while (waves < 16 && (int64_t)waves * 512 * most < cols) waves *= 4;
   const int64_t v = (cols + waves * 512 - 1) / (waves * 512);
   return {waves, v <= 1 ? 1 : (v <= 2 ? 2 : 4)};
@@ -339,19 +361,20 @@ NormShape shape_for(int64_t cols, int waves, int most) {
 
 }  // namespace
 
+// With few rows a row's latency counts: one vector a lane where waves allow.
 NormShape norm_forward_shape(int64_t rows, int64_t cols) {
-  (void)rows;
-  return shape_for(cols, 1, cols <= 1024 ? 2 : 4);
+  return shape_for(cols, rows <= 256 ? 1 : (cols <= 1024 ? 2 : 4));
 }
 NormShape norm_backward_shape(int64_t rows, int64_t cols) {
-  (void)rows;
-  return shape_for(cols, 1, cols <= 1024 ? 2 : 4);
+  return shape_for(cols, rows <= 256 ? 1 : (cols <= 1024 ? 2 : 4));
 }
 
+// A second kernel costs about as much as three rows one after another.
 int64_t norm_partial_rows(int64_t rows, int64_t cols, int cu_count) {
-  const NormShape s = norm_backward_shape(rows, cols);
-  const int64_t walkers = (int64_t)cu_count * 2 * rows_of(s.waves);
-  return rows < walkers ? rows : walkers;
+  const int at_once = rows_of(norm_backward_shape(rows, cols).waves);
+  if (rows <= 3 * at_once) return rows > 0 ? 1 : 0;
+  const int64_t groups = (rows + at_once - 1) / at_once, most = (int64_t)cu_count * 2;
+  return groups < most ? groups : most;
 }
 
 hipError_t launch_norm_forward(const NormArgs& a, bool e4m3, hipStream_t stream) {
@@ -373,12 +396,15 @@ hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream) {
     const norm_fn f = s.waves == 1 ? backward_pick<1>(s.vectors, res)
                                    : (s.waves == 4 ? backward_pick<4>(s.vectors, res)
                                                    : backward_pick<16>(s.vectors, res));
-    const int64_t grid = (a.partial_rows + rows_of(s.waves) - 1) / rows_of(s.waves);
-    hipLaunchKernelGGL(f, dim3((uint32_t)grid), dim3(threads_of(s.waves)), 0, stream, a);
+    hipLaunchKernelGGL(f, dim3((uint32_t)a.partial_rows), dim3(threads_of(s.waves)), 0, stream, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.partial_rows == 1) return e;
   }
-  hipLaunchKernelGGL(norm_sum_partials, dim3((uint32_t)((a.cols + 31) / 32)), dim3(1024), 0, stream, a);
+  // Few rows of sums: a thread a column.
+  if (a.partial_rows <= 16)
+    hipLaunchKernelGGL((norm_sum_partials<1, 64>), dim3((uint32_t)((a.cols + 63) / 64)), dim3(64), 0, stream, a);
+  else
+    hipLaunchKernelGGL((norm_sum_partials<32, 32>), dim3((uint32_t)((a.cols + 31) / 32)), dim3(1024), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -205,15 +205,34 @@ def _declare_plan_calls(lib, kind, desc):
 def _ptr(x) -> int | None:
     if x is None:
         return None
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
-    return int(x)
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return int(x)
+
+
+_current_stream = None
+
+
+def _find_current_stream():
+    """A call that returns the current torch stream's handle.  torch's public
+    one makes an object of it first, which takes longer (2.8 us) than a small
+    kernel's launch; it is used where torch lacks the short way (0.1 us)."""
+    global _current_stream
+    import torch
+    torch.cuda.current_stream()  # torch's device state exists from here on
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: int(torch.cuda.current_stream().cuda_stream)  # noqa: E731
+    return _current_stream
 
 
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return (_current_stream or _find_current_stream())()
     if hasattr(s, "cuda_stream"):
         return int(s.cuda_stream)
     return int(s)
@@ -347,8 +366,8 @@ def gemm_norm_desc_validate(desc: migemm_norm_desc) -> int:
 
 
 def gemm_norm_run(plan, x, r, weight, h, y, scale, rstd, stream=None, check: bool = True) -> int:
-    st = load().gemm_norm_run(_plan(plan), _ptr(x), _ptr(r), _ptr(weight), _ptr(h), _ptr(y),
-                              _ptr(scale), _ptr(rstd), _stream(stream))
+    st = (_lib or load()).gemm_norm_run(_plan(plan), _ptr(x), _ptr(r), _ptr(weight), _ptr(h), _ptr(y),
+                                        _ptr(scale), _ptr(rstd), _stream(stream))
     if check and st != MIGEMM_OK:
         raise MigemmError(st, "gemm_norm_run")
     return int(st)
@@ -356,7 +375,7 @@ def gemm_norm_run(plan, x, r, weight, h, y, scale, rstd, stream=None, check: boo
 
 def gemm_norm_run_backward(plan, dy, h, weight, rstd, dh, dx, dweight, workspace=None, stream=None,
                            check: bool = True) -> int:
-    st = load().gemm_norm_run_backward(_plan(plan), _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd),
+    st = (_lib or load()).gemm_norm_run_backward(_plan(plan), _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd),
                                        _ptr(dh), _ptr(dx), _ptr(dweight), _ptr(workspace),
                                        _stream(stream))
     if check and st != MIGEMM_OK:
@@ -370,7 +389,7 @@ def gemm_scaled_desc_validate(desc: migemm_scaled_desc) -> int:
 
 def gemm_scaled_run(plan, a, a_scale, b, b_scale, d, workspace=None, stream=None,
                     check: bool = True) -> int:
-    st = load().gemm_scaled_run(_plan(plan), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(d),
+    st = (_lib or load()).gemm_scaled_run(_plan(plan), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(d),
                                 _ptr(workspace), _stream(stream))
     if check and st != MIGEMM_OK:
         raise MigemmError(st, "gemm_scaled_run")
@@ -383,7 +402,7 @@ def gemm_vocab_loss_desc_validate(desc: migemm_vocab_loss_desc) -> int:
 
 def gemm_vocab_loss_run(plan, x, w, target, loss, lse, workspace=None, stream=None,
                         check: bool = True) -> int:
-    st = load().gemm_vocab_loss_run(_plan(plan), _ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse),
+    st = (_lib or load()).gemm_vocab_loss_run(_plan(plan), _ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse),
                                     _ptr(workspace), _stream(stream))
     if check and st != MIGEMM_OK:
         raise MigemmError(st, "gemm_vocab_loss_run")
@@ -392,7 +411,7 @@ def gemm_vocab_loss_run(plan, x, w, target, loss, lse, workspace=None, stream=No
 
 def gemm_vocab_loss_run_backward(plan, x, w, target, lse, dloss, dx, dw, workspace=None, stream=None,
                                  check: bool = True) -> int:
-    st = load().gemm_vocab_loss_run_backward(_plan(plan), _ptr(x), _ptr(w), _ptr(target), _ptr(lse),
+    st = (_lib or load()).gemm_vocab_loss_run_backward(_plan(plan), _ptr(x), _ptr(w), _ptr(target), _ptr(lse),
                                              _ptr(dloss), _ptr(dx), _ptr(dw), _ptr(workspace),
                                              _stream(stream))
     if check and st != MIGEMM_OK:
