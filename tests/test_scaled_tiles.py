@@ -78,3 +78,14 @@ def test_a_plan_with_split_sums_needs_its_workspace():
     a = [p.a.data_ptr(), p.sa.data_ptr(), p.b.data_ptr(), p.sb.data_ptr(), p.d.data_ptr()]
     assert lib.gemm_scaled_run(plan, *a, None, None) == migemm.MIGEMM_ERR_INVALID_ARG
     assert lib.gemm_scaled_run(plan, *a, p.ws.data_ptr() + 16, None) == migemm.MIGEMM_ERR_MISALIGNED
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(4000, 3000, 1000), (1500, 6000, 513), (2900, 4100, 2057), (193 * 16, 8192, 300),
+                                   (5000, 5000, 257)])
+def test_large_tiles_of_both_heights(M, N, K):
+    """192 and 256 rows a tile, with rows, columns and K past the last whole one."""
+    p = Scaled(M, N, K, seed=M + N + K)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()

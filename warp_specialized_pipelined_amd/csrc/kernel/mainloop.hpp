@@ -173,7 +173,7 @@ __device__ __forceinline__ int swz_k8(int row) { return (row >> 1) & 7; }
 template <int ES, bool KMAJ, int NL = 8>
 struct StageLoader {
   typedef StageGeom<ES> G;
-  static_assert(NL == 8 || (NL == 6 && ES == 2), "192-row operand tiles are bf16 only");
+  static_assert(NL == 8 || (NL == 6 && (ES == 2 || KMAJ)), "192-row operand tiles: bf16, or K-contiguous");
   const unsigned char* tile_base;  // operand address of the tile's (row 0, k 0)
   int64_t kstep_bytes;             // address step from one stage of K to the next
   int64_t bytes_left;              // operand bytes from tile_base to its end
@@ -319,8 +319,8 @@ struct FragReader<2, true, NB> {
 // K-contiguous e4m3: two ds_read_b128 per fragment, the two 16-byte halves
 // of the lane's 32 bytes of K: k-step ks, half h is chunk 4 ks + 2 (lane /
 // 32) + h.
-template <>
-struct FragReader<1, true> {
+template <int NB>
+struct FragReader<1, true, NB> {
   static constexpr int kReads = 2;
   uint32_t off[2][2];  // per k-step and half
   __device__ __forceinline__ void init(int row0, int lane) {
@@ -514,11 +514,13 @@ struct Frags {
 // path serves the four waves in turn, so loads packed closer than about 64
 // cycles stall the MFMA stream.
 //
-// 192-row tiles (BM = 3, bf16 only): 12 MFMAs per k-step and 6 A loads per
-// wave and stage.  The stage's 8 B loads no longer fit behind every other
-// MFMA of the first k-step: 6 go there, and the last 2 (kBEarly) are issued
-// one stage ahead, in the last k-step of the iteration before (into the
-// slot its barrier frees), behind the MFMAs the A loads leave free.
+// 192-row tiles (BM = 3): 12 MFMAs per k-step and 6 A loads per wave and
+// stage.  bf16: the stage's 8 B loads no longer fit behind every other MFMA of
+// the first k-step: 6 go there, and the last 2 (kBEarly) are issued one stage
+// ahead, in the last k-step of the iteration before (into the slot its
+// barrier frees), behind the MFMAs the A loads leave free.  e4m3
+// (K-contiguous operands only): the 14 loads share 12 MFMAs, two behind two
+// of them.
 //
 // mainloop_range runs K stages [k0, k0 + KT) of the tile (a stream-K
 // segment); K is the problem's K or, for a segment that ends before it, the
@@ -530,7 +532,7 @@ __device__ __forceinline__ void mainloop_range(Accum& acc, const KernelArgs& a, 
                                                int64_t K) {
   typedef StageGeom<ES> G;
   typedef Frags<ES, AK, BK, BM> FW;
-  static_assert(BM == 4 || (BM == 3 && ES == 2), "192-row tiles are bf16 only");
+  static_assert(BM == 4 || (BM == 3 && (ES == 2 || (AK && BK))), "192-row tiles: bf16, or K-contiguous operands");
   static_assert(BM == 4 || !SideWork::kLoadsC, "C is read in the K loop of 256-row tiles only");
   constexpr bool kBf16 = ES == 2;
   constexpr int kLast = G::kKSteps - 1;
@@ -582,7 +584,7 @@ __device__ __forceinline__ void mainloop_range(Accum& acc, const KernelArgs& a, 
       wait_vmcnt<2 * BM + kBEarly>();  // stage 0 has landed
     } else {
       lb.load_all(k0 + 1, kStageBytes + kB, K, wave);
-      wait_vmcnt<16>();
+      wait_vmcnt<2 * BM + 8>();
     }
     clear_tail(0, 0);
     barrier();
@@ -676,8 +678,12 @@ __device__ __forceinline__ void mainloop_range(Accum& acc, const KernelArgs& a, 
           }
         });
       } else {
-        if constexpr (m < 8) la.template load<kMask>(ra, krem_a, cur, wave, m);
-        else lb.template load<kMask>(rb, krem_b, cur + kB, wave, m - 8);
+        constexpr int kStageLoads = 2 * BM + 8;  // A's, then B's
+        static_for<m * kStageLoads / kM, (m + 1) * kStageLoads / kM>([&](auto xc) {
+          constexpr int x = decltype(xc)::value;
+          if constexpr (x < 2 * BM) la.template load<kMask>(ra, krem_a, cur, wave, x);
+          else lb.template load<kMask>(rb, krem_b, cur + kB, wave, x - 2 * BM);
+        });
       }
     });
   };

@@ -59,10 +59,10 @@ struct ScaledArgs {
   int32_t splits;
 };
 
-// Which kernel takes a product, into how many ranges K is split, and the
-// workspace that takes.
+// Which kernel takes a product, into how many ranges K is split, the height
+// of its tiles where it takes them one after another, and the workspace.
 struct ScaledChoice {
-  int variant, splits;
+  int variant, splits, tile_m;
   int64_t workspace_bytes;
 };
 ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count);

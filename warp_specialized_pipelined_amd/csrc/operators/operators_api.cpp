@@ -124,10 +124,10 @@ int check_workspace(size_t bytes, const void* workspace) {
   return aligned(workspace, 256) ? MIGEMM_OK : MIGEMM_ERR_MISALIGNED;
 }
 
-// The 256 x 256 tiles of an M x N product and their order, as the GEMM's plan
-// lays them out.
-void set_tiles(migemm::KernelArgs& a) {
-  a.tiles_m = (int32_t)((a.M + migemm::kTileM - 1) / migemm::kTileM);
+// The tile_m x 256 tiles of an M x N product and their order, as the GEMM's
+// plan lays them out.
+void set_tiles(migemm::KernelArgs& a, int tile_m = migemm::kTileM) {
+  a.tiles_m = (int32_t)((a.M + tile_m - 1) / tile_m);
   a.tiles_n = (int32_t)((a.N + migemm::kTileN - 1) / migemm::kTileN);
   a.num_tiles = a.tiles_per_batch = a.tiles_m * a.tiles_n;
   a.group_m = a.tiles_m < 8 ? (a.tiles_m > 0 ? a.tiles_m : 1) : 8;
@@ -392,8 +392,8 @@ int gemm_scaled_plan_create(const migemm_scaled_desc* desc, migemm_scaled_plan**
   a.lda = desc->a_rs, a.ldb = desc->b_cs, a.ldd = desc->d_rs;
   a.a_bytes = a.M > 0 ? (a.M - 1) * a.lda + a.K : 0;
   a.b_bytes = a.N > 0 ? (a.N - 1) * a.ldb + a.K : 0;
-  set_tiles(a);
   const migemm::ScaledChoice c = migemm::choose_scaled(a.M, a.N, a.K, cus);
+  set_tiles(a, c.tile_m);
   p->variant = c.variant;
   p->base.splits = c.splits;
   p->workspace_bytes = (size_t)c.workspace_bytes;

@@ -3,7 +3,7 @@
 //   d[m][n] = bf16(a_scale[m] b_scale[n] sum_k a[m][k] b[n][k])
 // a and b are e4m3 codes, K-contiguous; the sum is fp32.
 //
-// scaled_tile: 256 x 256 tiles with the GEMM's K loop, where the product fills
+// scaled_tile: 256 x 256 or 192 x 256 tiles with the GEMM's K loop, where the product fills
 // the chip with them (bound by the matrix instructions).  scaled_mid: smaller
 // tiles, their K split where there are few (bound by loads into LDS).
 // scaled_rows: tiles of 16 to 64 rows whose waves split K (bound by reading
@@ -27,6 +27,38 @@
 namespace migemm {
 namespace {
 
+// Row scales and column scales of a wave's 32 BM x 32 BN part at (m0, n0).
+// Scales past the matrix read as zero; what they scale is not stored.
+template <int BM, int BN>
+struct Scales {
+  float rows[BM];
+  f32x4 cols[BN][4];
+  __device__ __forceinline__ void load(const ScaledArgs& s, int64_t m0, int64_t n0, int lane) {
+    auto vec = [](const float* p, int64_t from, int64_t n) {
+      int64_t left = (n - from) * 4;
+      left = left < 0 ? 0 : (left > 512 ? 512 : left);
+      return make_rsrc(p + from, (uint32_t)left);
+    };
+    const __amdgpu_buffer_rsrc_t ra = vec(s.a_scale, m0, s.gemm.M), rb = vec(s.b_scale, n0, s.gemm.N);
+#pragma unroll
+    for (int i = 0; i < BM; ++i)
+      rows[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, (32 * i + (lane & 31)) * 4, 0, 0));
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        cols[j][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   rb, (32 * j + 8 * q + 4 * (lane >> 5)) * 4, 0, 0));
+  }
+  __device__ __forceinline__ f32x4 apply(f32x4 v, int bi, int bj, int q) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = v[c] * rows[bi] * cols[bj][q][c];
+    return v;
+  }
+};
+
+// 64 BM x 256 tiles, one after another.
+template <int BM>
 __global__ __launch_bounds__(kThreads, 1) void scaled_tile(ScaledArgs s) {
   const int lane0 = threadIdx.x & 63, wave0 = wave_id();
   const KernelArgs& a = s.gemm;
@@ -37,32 +69,14 @@ __global__ __launch_bounds__(kThreads, 1) void scaled_tile(ScaledArgs s) {
     int lane = lane0, wave = wave0;
     asm volatile("" : "+v"(lane));  // per-lane offsets are formed per tile, not held across tiles
     asm volatile("" : "+s"(wave));
-    mainloop<1, true, true>(acc, a, t.tm, t.tn, wave, lane, none);
-    const int64_t m0 = (int64_t)t.tm * kTileM + (wave >> 1) * kWaveTile;
+    mainloop<1, true, true, BM>(acc, a, t.tm, t.tn, wave, lane, none);
+    const int64_t m0 = (int64_t)t.tm * (64 * BM) + (wave >> 1) * (32 * BM);
     const int64_t n0 = (int64_t)t.tn * kTileN + (wave & 1) * kWaveTile;
-    // Scales past the matrix read as zero; what they scale is not stored.
-    auto vec = [](const float* p, int64_t from, int64_t n) {
-      int64_t left = (n - from) * 4;
-      left = left < 0 ? 0 : (left > 512 ? 512 : left);
-      return make_rsrc(p + from, (uint32_t)left);
-    };
-    const __amdgpu_buffer_rsrc_t ra = vec(s.a_scale, m0, a.M), rb = vec(s.b_scale, n0, a.N);
-    float rows[4];
-    f32x4 cols[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rows[i] = __uint_as_float(
-          __builtin_amdgcn_raw_buffer_load_b32(ra, (32 * i + (lane & 31)) * 4, 0, 0));
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        cols[i][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                   rb, (32 * i + 8 * q + 4 * (lane >> 5)) * 4, 0, 0));
-    }
-    tile_store<true>(a.D, a.ldd, a.M, a.N, m0, n0, wave, lane, [&](int bi, int bj, int q) {
-      f32x4 v;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = acc.v[bi][bj][4 * q + c] * rows[bi] * cols[bj][q][c];
-      return v;
+    Scales<BM, 4> scales;
+    scales.load(s, m0, n0, lane);
+    tile_store<true, BM>(a.D, a.ldd, a.M, a.N, m0, n0, wave, lane, [&](int bi, int bj, int q) {
+      const f32x16& v = acc.v[bi][bj];
+      return scales.apply(f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}, bi, bj, q);
     });
     wait_lgkmcnt<0>();  // staging reads done ...
     barrier();          // ... in every wave before the ring is refilled
@@ -95,36 +109,6 @@ __global__ __launch_bounds__(64 * W) void scaled_rows(ScaledArgs s) {
     store4(static_cast<unsigned short*>(a.D) + m * a.ldd + n, a.N - n, v);
   });
 }
-
-// Row scales and column scales of a wave's 32 BM x 32 BN part at (m0, n0).
-// Scales past the matrix read as zero; what they scale is not stored.
-template <int BM, int BN>
-struct Scales {
-  float rows[BM];
-  f32x4 cols[BN][4];
-  __device__ __forceinline__ void load(const ScaledArgs& s, int64_t m0, int64_t n0, int lane) {
-    auto vec = [](const float* p, int64_t from, int64_t n) {
-      int64_t left = (n - from) * 4;
-      left = left < 0 ? 0 : (left > 512 ? 512 : left);
-      return make_rsrc(p + from, (uint32_t)left);
-    };
-    const __amdgpu_buffer_rsrc_t ra = vec(s.a_scale, m0, s.gemm.M), rb = vec(s.b_scale, n0, s.gemm.N);
-#pragma unroll
-    for (int i = 0; i < BM; ++i)
-      rows[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, (32 * i + (lane & 31)) * 4, 0, 0));
-#pragma unroll
-    for (int j = 0; j < BN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        cols[j][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                   rb, (32 * j + 8 * q + 4 * (lane >> 5)) * 4, 0, 0));
-  }
-  __device__ __forceinline__ f32x4 apply(f32x4 v, int bi, int bj, int q) const {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = v[c] * rows[bi] * cols[bj][q][c];
-    return v;
-  }
-};
 
 // TM x TN tiles (midtile.hpp), a workgroup for each of a tile's `splits`
 // ranges of K stages.  With one it stores the result; with more each stores
@@ -210,16 +194,17 @@ constexpr Variant mid_variant(int per_cu, double stage1, double stage2, double t
   return {TM, TN, 256, (int)MidGeom<TM, TN, SLOTS>::kLds, scaled_mid<EXACT, TM, TN, SLOTS>,
           EXACT ? nullptr : scaled_join<TM, TN>, per_cu, stage1, stage2, tile};
 }
-enum { kTile256, kRowsFirst, kRowsLast = 4, kMidFirst, kMidLast = 7, kExactRows, kExactMid };
+enum { kTile256, kTile192, kRowsFirst, kRowsLast = 5, kMidFirst, kMidLast = 8, kExactRows, kExactMid };
 const Variant kVariants[] = {
-    {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile, nullptr, 1, 1.0, 1.0, 6.0},
+    {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile<4>, nullptr, 1, 1.1, 1.1, 7.0},
+    {kTileMShort, kTileN, kThreads, kPlainLdsBytes, scaled_tile<3>, nullptr, 1, 0.95, 0.95, 6.0},
     rows_variant<1, 1, 1, 16, 2>(1),
     rows_variant<1, 1, 2, 16, 1>(2),
     rows_variant<1, 2, 2, 8, 1>(2),
     rows_variant<1, 4, 2, 8, 1>(2),
     mid_variant<false, 64, 64, 4>(2, 0.30, 0.48, 1.7),
     mid_variant<false, 64, 128, 3>(2, 0.39, 0.62, 1.3),
-    mid_variant<false, 128, 128, 4>(1, 0.46, 0.46, 2.7),
+    mid_variant<false, 128, 128, 4>(1, 0.52, 0.52, 2.4),
     rows_variant<kExactE4M3, 1, 4, 2, 1>(2),
     mid_variant<true, 64, 64, 2>(2, 0, 0, 0),
 };
@@ -248,27 +233,29 @@ double cost_of(const Variant& v, bool rows, int64_t M, int64_t N, int64_t K, int
 
 }  // namespace
 
-// The kernel that costs least: the figures are a fit to 500 products of 1 to
+// The kernel that costs least: the figures are a fit to 450 products of 1 to
 // 8192 rows, 64 to 8192 columns and K of 257 to 16384, each timed with every
 // kernel and up to eight splits; what it picks is 2.5% slower than the fastest
 // of them on average.
 ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count) {
   // Short sums in exact products: with two K steps at most the time goes into
   // launch and output, whichever instruction multiplies.
-  if (K <= 256) return {M <= 16 ? kExactRows : kExactMid, 1, 0};
-  ScaledChoice best = {kTile256, 1, 0};
-  // (Every tile count fits 31 bits for the variants tried.)
-  double least = cost_of(kVariants[kTile256], false, M, N, K, 1, cu_count);
-  if ((double)M * N > 1e9) return best;
-  for (int i = kRowsFirst; i <= kMidLast; ++i)
+  if (K <= 256) return {M <= 16 ? kExactRows : kExactMid, 1, kTileM, 0};
+  ScaledChoice best = {kTile256, 1, kTileM, 0};
+  double least = 1e300;
+  // (Past 2^30 results only the large tiles, whose count stays within 31 bits.)
+  const int last = (double)M * N > 1e9 ? kTile192 : kMidLast;
+  for (int i = kTile256; i <= last; ++i)
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (splits > 1 && (i <= kRowsLast || K < 128 * 3 * splits)) break;
-      const double cost = cost_of(kVariants[i], i <= kRowsLast, M, N, K, splits, cu_count);
+      if (splits > 1 && (i < kMidFirst || K < 128 * 3 * splits)) break;
+      const double cost =
+          cost_of(kVariants[i], i >= kRowsFirst && i <= kRowsLast, M, N, K, splits, cu_count);
       if (cost >= least) continue;
       least = cost;
-      best = {i, splits, 0};
+      best = {i, splits, kTileM, 0};
     }
   const Variant& v = kVariants[best.variant];
+  best.tile_m = v.tm;
   if (best.splits > 1) best.workspace_bytes = tiles_of(v, M, N) * best.splits * v.tm * v.tn * 4;
   return best;
 }
@@ -286,7 +273,7 @@ hipError_t prepare_scaled() {
 hipError_t launch_scaled(const ScaledArgs& s, int variant, int cu_count, hipStream_t stream) {
   const Variant& v = kVariants[variant];
   const int64_t tiles = tiles_of(v, s.gemm.M, s.gemm.N);
-  const int64_t grid = variant == kTile256 ? (tiles < cu_count ? tiles : cu_count) : tiles * s.splits;
+  const int64_t grid = variant <= kTile192 ? (tiles < cu_count ? tiles : cu_count) : tiles * s.splits;
   hipLaunchKernelGGL(v.kernel, dim3((uint32_t)grid), dim3(v.threads), v.lds, stream, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.splits == 1) return e;

@@ -1,5 +1,5 @@
-// tile_store.hpp -- a wave's 128 x 128 quarter of a 256 x 256 tile, each
-// value transformed, rounded to bf16, staged through LDS and stored to a
+// tile_store.hpp -- a wave's 128 x 128 quarter of a 256 x 256 tile (BM = 3: 96
+// x 128 of a 192 x 256 tile), each value transformed, rounded to bf16, staged through LDS and stored to a
 // row-major matrix with 16-byte stores (the layout and the order of accesses
 // are those of the GEMM's epilogue).
 #pragma once
@@ -11,13 +11,13 @@ namespace migemm {
 // value(bi, bj, q) gives the four results of row 32 bi + l % 32, columns
 // 32 bj + 8 q + 4 (l / 32) .. + 3 of the wave's quarter.  NT: stores carry the
 // non-temporal hint (for results not read again soon).
-template <bool NT, class Value>
+template <bool NT, int BM = 4, class Value>
 __device__ __forceinline__ void tile_store(void* D, int64_t ldd, int64_t M, int64_t N, int64_t m0,
                                            int64_t n0, int wave, int lane, Value&& value) {
   const int lr = lane & 31, half = lane >> 5;
   const uint32_t st_base = wave * kStagingWaveBytes + lr * kStagingRowBytes + 8 * half;
 #pragma unroll
-  for (int bi = 0; bi < 4; ++bi)
+  for (int bi = 0; bi < BM; ++bi)
 #pragma unroll
     for (int bj = 0; bj < 4; ++bj)
 #pragma unroll
@@ -34,7 +34,7 @@ __device__ __forceinline__ void tile_store(void* D, int64_t ldd, int64_t M, int6
   const uint32_t rd_base = wave * kStagingWaveBytes + rsub * kStagingRowBytes + chunk * 16;
   const uint32_t d_lane = (uint32_t)((rsub * ldd + 8 * chunk) * 2);
 #pragma unroll 8
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < 8 * BM; ++i) {
     const u32x4 v = *(const MIGEMM_LDS u32x4*)lds_at(rd_base + 4 * i * kStagingRowBytes);
     const int row = 4 * i + rsub;
     if (row < rows_left && cols_left > 0) {
