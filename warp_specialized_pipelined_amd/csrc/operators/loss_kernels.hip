@@ -222,7 +222,9 @@ __global__ __launch_bounds__(1024) void loss_gather_rows(LossArgs s, int64_t row
   __shared__ float tops[16];
   __shared__ int places[1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t begin = (int64_t)blockIdx.x * rows;
+  // (The last workgroups may have no rows: nothing past T is read either.)
+  const int64_t from_row = (int64_t)blockIdx.x * rows;
+  const int64_t begin = from_row < s.T ? from_row : s.T;
   const int64_t end = begin + rows < s.T ? begin + rows : s.T;
   auto counts = [&](int64_t t) { return t >= 0 && t < s.V; };
   auto add_up = [&](int n) {
