@@ -24,7 +24,7 @@ def test_loss_and_gradients(T, V, H):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,V,H", [(40, 3000, 100), (1282, 200, 64), (5, 20000, 70)])
+@pytest.mark.parametrize("T,V,H", [(40, 3000, 100), (1282, 200, 64), (20, 20000, 70)])
 def test_rows_that_hold_anything_reach_nothing(T, V, H):
     p, q = Loss(T, V, H, seed=5), Loss(T, V, H, seed=5)
     dead = p.target < 0

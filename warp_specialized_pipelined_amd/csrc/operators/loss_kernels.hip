@@ -16,11 +16,12 @@
 // logits are formed again, g of the piece is stored as bf16, and two products
 // read it: dw of the piece, complete, and the piece's share of dx, added up
 // in fp32.  g is the one quantity rounded to bf16 in between: the matrix
-// instructions take bf16 pairs.  It is stored as a multiple of the largest
-// |dloss|, and the products are scaled back in fp32: where dloss is the same
-// in every row, as for a mean, the one-hot part, which makes up nearly all of
-// g, is then exactly -1, and what is rounded (half a step, 2^-9 on average, of
-// each exp(logits - lse)) is far below the rounding of the outputs.
+// instructions take bf16 pairs.  It is divided by the significand of the
+// largest |dloss|, and the products are multiplied by it in fp32: where dloss
+// is the same in every row, as for a mean, the one-hot part, which makes up
+// nearly all of g, is then a power of two, and what is rounded (half a step,
+// 2^-9 on average, of each exp(logits - lse)) is far below the rounding of the
+// outputs.
 //
 // The tiles are 256 x 256 with the GEMM's K loop, or 128 x 128 or 64 x 64
 // (midtile.hpp) where those are too few or too large; in the backward pass
@@ -216,7 +217,8 @@ __global__ __launch_bounds__(1024) void loss_join(LossArgs s) {
 // together: x, with what their gradient needs; zeros in dx for the others.
 // from[number] is the row.  Each workgroup takes `rows` consecutive rows, and
 // counts the targets before them itself; the first one also counts them all
-// and finds the largest |dloss|.  A wave copies a row.
+// and finds the largest |dloss|, whose significand (1 .. 2) is the gradients'
+// factor.  A wave copies a row.
 __global__ __launch_bounds__(1024) void loss_gather_rows(LossArgs s, int64_t rows) {
   __shared__ int totals[16];
   __shared__ float tops[16];
@@ -256,8 +258,9 @@ __global__ __launch_bounds__(1024) void loss_gather_rows(LossArgs s, int64_t row
     __syncthreads();
     if (threadIdx.x == 0) {
       for (int w = 1; w < 16; ++w) top = fmaxf(top, tops[w]);
+      int exponent;
       s.head->count = n;
-      s.head->top = top > 0.0f ? top : 1.0f;
+      s.head->factor = top > 0.0f ? 2.0f * frexpf(top, &exponent) : 1.0f;
     }
   }
   int base = 0;
@@ -319,12 +322,12 @@ __device__ __forceinline__ KernelArgs with_rows(const LossArgs& s, KernelArgs a)
 }
 
 // The wave's logits of rows m0.., columns n0.. of the piece (first_col ..) made
-// g, as a multiple of the largest |dloss|.
+// g over the factor.
 template <int BM, int BN>
 __device__ __forceinline__ void logits_to_gradient(f32x16 (&v)[BM][BN], const LossArgs& s, int64_t rows,
                                                    int64_t m0, int64_t n0, int lane) {
   const int lr = lane & 31, half = lane >> 5;
-  const float top = s.head->top;
+  const float factor = s.head->factor;
   float lse[BM], scale[BM];
   int want[BM];  // the target's column here, or -1
 #pragma unroll
@@ -332,7 +335,7 @@ __device__ __forceinline__ void logits_to_gradient(f32x16 (&v)[BM][BN], const Lo
     const int64_t row = m0 + 32 * bi + lr;
     const bool in = row < rows;
     lse[bi] = in ? s.rows_lse[row] : 0.0f;
-    scale[bi] = in ? s.rows_dloss[row] / top : 0.0f;
+    scale[bi] = in ? s.rows_dloss[row] / factor : 0.0f;
     const int64_t at = in ? (int64_t)s.rows_target[row] - s.first_col - n0 : -1;
     want[bi] = at >= 0 && at < 32 * BN ? (int)at : -1;
   }
@@ -407,7 +410,7 @@ __global__ __launch_bounds__(kThreads, 1) void loss_dw_tiles(LossArgs s) {
   const int lane = threadIdx.x & 63, wave = wave_id();
   KernelArgs a = s.gemm;
   const int count = s.head->count;
-  const float top = s.head->top;
+  const float factor = s.head->factor;
   a.K = count;
   a.a_bytes = count > 0 ? ((int64_t)(count - 1) * a.lda + a.M) * 2 : 0;
   a.b_bytes = count > 0 ? ((int64_t)(count - 1) * a.ldb + a.N) * 2 : 0;
@@ -420,7 +423,7 @@ __global__ __launch_bounds__(kThreads, 1) void loss_dw_tiles(LossArgs s) {
     const Ids ie(lane, wave);
     tile_store<true>(a.D, a.ldd, a.M, a.N, (int64_t)t.tm * kTileM + (ie.wave >> 1) * kWaveTile,
                      (int64_t)t.tn * kTileN + (ie.wave & 1) * kWaveTile, ie.wave, ie.lane,
-                     [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * top; });
+                     [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * factor; });
     wait_lgkmcnt<0>();
     barrier();
   }
@@ -476,7 +479,7 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
   typedef MidGeom<TM, TN, SLOTS> G;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int count = s.head->count;
-  const float top = s.head->top;
+  const float factor = s.head->factor;
   const int dx_tiles_m = (int)((s.T + TM - 1) / TM), tiles_n = (int)((s.H + TN - 1) / TN);
   const int dx_tiles = dx_tiles_m * tiles_n, dx_items = s.dx_items;
   const int slot = persistent_slot(blockIdx.x, gridDim.x);
@@ -498,7 +501,7 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
       mid_store<G::kBM, G::kBN>(
           a.D, a.ldd, a.M, a.N, (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM,
           (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN, wave, lane,
-          [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * top; },
+          [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * factor; },
           [&](int64_t r) { return (int64_t)s.from[r]; });
     }
   } else {
@@ -520,7 +523,7 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
       mid_store<G::kBM, G::kBN>(
           a.D, a.ldd, a.M, a.N, (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM,
           (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN, wave, lane,
-          [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * top; }, [](int64_t r) { return r; });
+          [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q) * factor; }, [](int64_t r) { return r; });
     }
   }
 }
@@ -542,7 +545,7 @@ __global__ __launch_bounds__(64) void loss_finish(LossArgs s, int dx_blocks) {
   const int64_t m = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM + 32 * (block / BN) + (lane & 31);
   const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN + 32 * (block % BN);
   if (m >= M || n0 >= s.H) return;
-  const float top = s.head->top;
+  const float factor = s.head->factor;
   MidAccum<1, 1> acc = {};
   const int splits = dx ? s.splits : s.dw_splits;
   const mid_piece* sums = dx ? s.dx_sums : s.dw_sums;
@@ -553,7 +556,7 @@ __global__ __launch_bounds__(64) void loss_finish(LossArgs s, int dx_blocks) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int64_t n = n0 + 8 * q + 4 * (lane >> 5);
-    store4(d + n, s.H - n, quarter_of(acc.v[0][0], q) * top);
+    store4(d + n, s.H - n, quarter_of(acc.v[0][0], q) * factor);
   }
 }
 

@@ -73,8 +73,8 @@ hipError_t launch_scaled(const ScaledArgs& a, int variant, int cu_count, hipStre
 
 // What the backward pass finds out about its rows.
 struct LossHead {
-  int count;  // rows that count
-  float top;  // the largest |dloss| of theirs, or 1
+  int count;     // rows that count
+  float factor;  // the significand (1 .. 2) of the largest |dloss| of theirs, or 1
 };
 
 struct LossArgs {
