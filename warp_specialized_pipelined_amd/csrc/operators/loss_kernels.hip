@@ -23,9 +23,10 @@
 // 2^-9 on average, of each exp(logits - lse)) is far below the rounding of the
 // outputs.
 //
-// The tiles are 256 x 256 with the GEMM's K loop, or 128 x 128 or 64 x 64
+// The tiles are 256 x 256 with the GEMM's K loop, or 128 or 64 rows and columns
 // (midtile.hpp) where those are too few or too large; in the backward pass
-// the small tiles' two products share a launch and K is split.
+// the small tiles' two products share a launch and K is split.  Very few
+// logits with much K take 16 x 32 tiles whose waves split K.
 //
 // Bound: the matrix instructions (one product forward, three backward), or
 // for small ones launches and latency.
@@ -163,6 +164,45 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_forward_mi
                                          (int)((a.K + 63) / 64), a.K);
   reduce_logits(acc.v, s, (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM,
                 (int64_t)t.tn * TN + (wave & 1) * 32 * G::kBN, lane);
+}
+
+// Few tiles and much K: 16 x 32 tiles whose 16 waves split K (rowblock.hpp).
+constexpr int kRowsNB = 2, kRowsWaves = 16;
+template <class Done>
+__device__ __forceinline__ void rows_tile(const KernelArgs& a, int64_t m0, int64_t n0, f32x4* part, int wave,
+                                          int lane, Done&& done) {
+  RowBlock<1> ra;
+  RowBlock<kRowsNB> rb;
+  ra.init(a.A, a.lda * 2, a.M, m0, a.K * 2, lane);
+  rb.init(a.B, a.ldb * 2, a.N, n0, a.K * 2, lane);
+  f32x4 acc[1][kRowsNB] = {};
+  rowblock_loop<2, 1, kRowsNB, kRowsWaves, 1>(acc, ra, rb, a.K * 2, wave, lane);
+  rowblock_join<1, kRowsNB, kRowsWaves>(acc, part, wave, lane, [&](int, int nb, f32x4 v) {
+    done(m0 + (lane & 15), n0 + 16 * nb + 4 * (lane >> 4), v);
+  });
+}
+__global__ __launch_bounds__(64 * kRowsWaves) void loss_forward_rows(LossArgs s) {
+  __shared__ f32x4 part[kRowsWaves * kRowsNB * 64];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const KernelArgs& a = s.gemm;
+  const int tiles_m = (int)((a.M + 15) / 16), t = persistent_slot(blockIdx.x, gridDim.x);
+  rows_tile(a, (int64_t)(t % tiles_m) * 16, (int64_t)(t / tiles_m) * 32, part, wave, lane,
+            [&](int64_t m, int64_t n, f32x4 v) {
+              const int64_t left = a.N - n;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) v[c] = c < left ? v[c] : -INFINITY;
+              float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+              top = fmaxf(top, __shfl_xor(top, 16, 64));
+              top = fmaxf(top, __shfl_xor(top, 32, 64));
+              const float ref = reference_of(top);
+              float sum = (exp_diff(v[0], ref) + exp_diff(v[1], ref)) + (exp_diff(v[2], ref) + exp_diff(v[3], ref));
+              sum += __shfl_xor(sum, 16, 64);
+              sum += __shfl_xor(sum, 32, 64);
+              if (m >= a.M || (n & ~(int64_t)15) >= a.N) return;
+              if (lane < 16) s.parts[(n >> 4) * s.part_rows + m] = {top, sum};
+              const int64_t at = s.target[m] - n;
+              if (at >= 0 && at < 4 && at < left) s.target_logit[m] = v[at];
+            });
 }
 
 // A largest logit and the sum of exponentials against it (of them all).
@@ -404,6 +444,24 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_gradient_m
       [&](int bi, int bj, int q) { return quarter_of(acc.v[bi][bj], q); }, [](int64_t r) { return r; });
 }
 
+__global__ __launch_bounds__(64 * kRowsWaves) void loss_gradient_rows(LossArgs s) {
+  __shared__ f32x4 part[kRowsWaves * kRowsNB * 64];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int tiles_m = (int)((s.gemm.M + 15) / 16), t = persistent_slot(blockIdx.x, gridDim.x);
+  const KernelArgs a = with_rows(s, s.gemm);
+  const float factor = s.head->factor;
+  const int64_t m0 = (int64_t)(t % tiles_m) * 16;
+  if (m0 >= a.M) return;
+  rows_tile(a, m0, (int64_t)(t / tiles_m) * 32, part, wave, lane, [&](int64_t m, int64_t n, f32x4 v) {
+    if (m >= a.M || n >= a.N) return;
+    const float lse = s.rows_lse[m], scale = s.rows_dloss[m] / factor;
+    const int64_t at = (int64_t)s.rows_target[m] - s.first_col - n;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = (exp_diff(v[c], lse) - (c == at ? 1.0f : 0.0f)) * scale;
+    store4(static_cast<unsigned short*>(a.D) + m * a.ldd + n, a.N - n, v);
+  });
+}
+
 // dw of the piece = g^T x: rows are the piece's vocabulary, K the rows that
 // count.
 __global__ __launch_bounds__(kThreads, 1) void loss_dw_tiles(LossArgs s) {
@@ -482,9 +540,13 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
   const float factor = s.head->factor;
   const int dx_tiles_m = (int)((s.T + TM - 1) / TM), tiles_n = (int)((s.H + TN - 1) / TN);
   const int dx_tiles = dx_tiles_m * tiles_n, dx_items = s.dx_items;
-  const int slot = persistent_slot(blockIdx.x, gridDim.x);
+  // (Each product's parts are dealt over the XCDs by themselves: dx's are the
+  // longer ones, and few.)
+  const bool is_dx = (int)blockIdx.x < dx_items;
+  const int slot = is_dx ? persistent_slot(blockIdx.x, dx_items)
+                         : persistent_slot(blockIdx.x - dx_items, gridDim.x - dx_items);
   MidAccum<G::kBM, G::kBN> acc;
-  if (slot < dx_items) {
+  if (is_dx) {
     const KernelArgs a = with_rows(s, s.gemm_dx);
     const int split = slot / dx_tiles;
     const MidTile t = mid_tile(slot - split * dx_tiles, dx_tiles_m, tiles_n);
@@ -510,15 +572,15 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
     a.a_bytes = count > 0 ? ((int64_t)(count - 1) * a.lda + a.M) * 2 : 0;
     a.b_bytes = count > 0 ? ((int64_t)(count - 1) * a.ldb + a.N) * 2 : 0;
     const int tiles_m = (int)((a.M + TM - 1) / TM), tiles = tiles_m * tiles_n;
-    const int split = (slot - dx_items) / tiles;
-    const MidTile t = mid_tile(slot - dx_items - split * tiles, tiles_m, tiles_n);
+    const int split = slot / tiles;
+    const MidTile t = mid_tile(slot - split * tiles, tiles_m, tiles_n);
     const int stages = (count + 63) / 64;
     const int k0 = (int)((int64_t)stages * split / s.dw_splits);
     const int k1 = (int)((int64_t)stages * (split + 1) / s.dw_splits);
     mid_loop<2, false, false, TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0,
                                              k1 - k0, k1 * 64 < count ? k1 * 64 : count);
     if (s.dw_splits > 1) {
-      mid_put(s.dw_sums, slot - dx_items, acc, wave, lane);
+      mid_put(s.dw_sums, slot, acc, wave, lane);
     } else {
       mid_store<G::kBM, G::kBN>(
           a.D, a.ldd, a.M, a.N, (int64_t)t.tm * TM + (wave >> 1) * 32 * G::kBM,
@@ -549,7 +611,7 @@ __global__ __launch_bounds__(64) void loss_finish(LossArgs s, int dx_blocks) {
   MidAccum<1, 1> acc = {};
   const int splits = dx ? s.splits : s.dw_splits;
   const mid_piece* sums = dx ? s.dx_sums : s.dw_sums;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < splits; ++i) mid_add<BM, BN>(sums, (int64_t)i * tiles_m * tiles_n + tile, acc, wave, block, lane);
   unsigned short* d = dx ? static_cast<unsigned short*>(s.dx) + (int64_t)s.from[m] * s.dx_rs
                          : static_cast<unsigned short*>(s.gemm.D) + m * s.gemm.ldd;
@@ -613,12 +675,18 @@ LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_co
   const int64_t W = piece < V ? piece : V, sh = (H + 63) / 64, sw = (W + 63) / 64, st = (T + 63) / 64;
   const double t = (double)T, v = (double)V, h = (double)H, w = (double)W;
   double least_f = 1e300, least_g = 1e300;
-  for (int i = 0; i < kLossTiles; ++i) {
+  for (int i = 0; i <= kLossRows; ++i) {
+    auto logits = [&](LossProduct what, int64_t cols, double bytes) {
+      if (i < kLossTiles) return cost_of(i, what, T, cols, sh, 1, bytes, cu_count).us;
+      // What a compute unit takes in, and the memory.
+      const double tiles = (double)loss_tiles(i, T, cols), rounds = tiles > cu_count ? tiles / cu_count : 1.0;
+      const double cu = rounds * (kLossTileM[i] + kLossTileN[i]) * 2 * h / 52e3, memory = bytes / 5.1e6;
+      return 3.0 + (cu > memory ? cu : memory) + 0.6 * ceil(tiles / (2 * cu_count));
+    };
     // (A row's pairs, one for half a tile's columns, are written and joined.)
-    const double f = cost_of(i, kForward, T, V, sh, 1, 2 * h * (t + v), cu_count).us +
-                     16 * t * (v / (kLossTileN[i] / 2)) / 4e6;
+    const double f = logits(kForward, V, 2 * h * (t + v)) + 16 * t * (v / (kLossTileN[i] / 2)) / 4e6;
     if (f < least_f) least_f = f, c.forward = i;
-    const double g = cost_of(i, kGradient, T, W, sh, 1, 2 * (h * (t + w) + t * w), cu_count).us;
+    const double g = logits(kGradient, W, 2 * (h * (t + w) + t * w));
     if (g < least_g) least_g = g, c.gradient = i;
   }
   // Both products' tiles and splits together: alike, they share the launches.
@@ -688,6 +756,8 @@ hipError_t launch_loss_forward(const LossArgs& s, int tile, int cu_count, hipStr
   const int64_t tiles = loss_tiles(tile, s.gemm.M, s.gemm.N);
   if (tile == kLoss256) {
     MIGEMM_LAUNCH(loss_forward_tiles, tiles < cu_count ? tiles : cu_count, kThreads, kPlainLdsBytes, s);
+  } else if (tile == kLossRows) {
+    MIGEMM_LAUNCH(loss_forward_rows, tiles, 64 * kRowsWaves, 0, s);
   } else {
     MIGEMM_LAUNCH(kMid[tile - 1].forward, tiles, 256, kMid[tile - 1].lds, s);
   }
@@ -707,6 +777,8 @@ hipError_t launch_loss_gradient(const LossArgs& s, int tile, int cu_count, hipSt
   const int64_t tiles = loss_tiles(tile, s.gemm.M, s.gemm.N);
   if (tile == kLoss256) {
     MIGEMM_LAUNCH(loss_gradient_tiles, tiles < cu_count ? tiles : cu_count, kThreads, kPlainLdsBytes, s);
+  } else if (tile == kLossRows) {
+    MIGEMM_LAUNCH(loss_gradient_rows, tiles, 64 * kRowsWaves, 0, s);
   } else {
     MIGEMM_LAUNCH(kMid[tile - 1].gradient, tiles, 256, kMid[tile - 1].lds, s);
   }

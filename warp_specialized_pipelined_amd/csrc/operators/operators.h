@@ -110,11 +110,11 @@ struct LossArgs {
   int32_t first_piece, dx_summed;
 };
 
-// Tiles of the loss's products: 256 x 256 (the GEMM's K loop) or smaller
-// (midtile.hpp).
-enum LossTile { kLoss256, kLoss128, kLoss64x128, kLoss64, kLossTiles };
-constexpr int kLossTileM[] = {256, 128, 64, 64};
-constexpr int kLossTileN[] = {256, 128, 128, 64};
+// Tiles of the loss's products: 256 x 256 (the GEMM's K loop), smaller
+// (midtile.hpp), and for the logits alone 16 x 32 (rowblock.hpp).
+enum LossTile { kLoss256, kLoss128, kLoss64x128, kLoss64, kLossTiles, kLossRows = kLossTiles };
+constexpr int kLossTileM[] = {256, 128, 64, 64, 16};
+constexpr int kLossTileN[] = {256, 128, 128, 64, 32};
 inline int64_t loss_tiles(int tile, int64_t rows, int64_t cols) {
   return ((rows + kLossTileM[tile] - 1) / kLossTileM[tile]) * ((cols + kLossTileN[tile] - 1) / kLossTileN[tile]);
 }
