@@ -432,7 +432,8 @@ int gemm_norm_run_backward(const migemm_norm_plan* plan, const void* dy, const v
  *   d[m][n] = bf16(a_scale[m] * b_scale[n] * sum over k of a[m][k] b[n][k])
  * a is M x K and b N x K e4m3 (both K-contiguous: b_cs is the stride between
  * the columns of the K x N operand), d M x N bf16; sums are fp32, rounded
- * once.  From one row to many: the plan chooses among kernels by the sizes.
+ * once.  From one row to many: the plan chooses among kernels by the sizes,
+ * and where it splits K a run needs a workspace for the parts' sums.
  * M, N and K may be 0 (K = 0: d is zero); 256 rows of a, b and d each span
  * less than 2^31 bytes (else UNSUPPORTED). */
 typedef struct migemm_scaled_desc {
@@ -464,8 +465,10 @@ int gemm_scaled_run(const migemm_scaled_plan* plan, const void* a, const float* 
  *   dx = bf16(g w),   dw = bf16(g^T x)
  * where a row whose target is not in [0, vocab) has g = 0 exactly, whatever
  * x and dloss hold there: its dx is 0, and it adds nothing to dw.  lse is
- * written for every row.  g is rounded to bf16 on its way into the two
- * products, whose sums are fp32.  rows may be 0, vocab and hidden are at
+ * written for every row.  g, over the significand of the largest |dloss| of
+ * the rows that count, is rounded to bf16 on its way into the two products,
+ * whose sums are fp32 (with one dloss for every row, as for a mean, the
+ * one-hot part is exact).  rows may be 0, vocab and hidden are at
  * least 1; rows and vocab below 2^28, and 256 rows of each matrix span less
  * than 2^31 bytes (else UNSUPPORTED). */
 typedef struct migemm_vocab_loss_desc {
@@ -482,8 +485,8 @@ int gemm_vocab_loss_desc_validate(const migemm_vocab_loss_desc* desc);
 int gemm_vocab_loss_plan_create(const migemm_vocab_loss_desc* desc, migemm_vocab_loss_plan** out);
 int gemm_vocab_loss_plan_destroy(migemm_vocab_loss_plan* plan);
 /* Bytes of workspace either run needs (256-byte aligned).  Forward: 8 bytes a
- * row (of up to 16384) and 128 vocabulary entries.  Backward: the rows that
- * count, one piece of g (up to 512 MiB) and fp32 sums of dx. */
+ * row (of up to 16384) and 16 to 128 vocabulary entries.  Backward: the rows
+ * that count, one piece of g (up to 512 MiB) and fp32 sums of dx and dw. */
 size_t gemm_vocab_loss_workspace_size(const migemm_vocab_loss_plan* plan);
 
 /* target is int64 [rows]; loss and lse are fp32 [rows]. */

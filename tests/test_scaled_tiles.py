@@ -89,3 +89,31 @@ def test_large_tiles_of_both_heights(M, N, K):
     p.run()
     torch.cuda.synchronize()
     p.check()
+
+
+@pytest.mark.gpu
+def test_more_tiles_than_a_launch_has_threads_for():
+    """8400 x 4190000 results of a short sum: their 64 x 64 tiles of 256
+    threads come in more than one launch.  Whole numbers: exact."""
+    M, N, K = 8400, 4_190_000, 16
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB")
+    a = torch.ones((M, K), device="cuda").to(torch.float8_e4m3fn)
+    col = torch.arange(N, device="cuda")
+    value = torch.tensor([0.0, 1.0, -1.0, 2.0], device="cuda")
+    b = torch.ones((N, K), device="cuda")
+    b[:, 5] = value[col % 4]
+    b[:, 15] = value[(col // 7) % 4]
+    total = b.sum(1)
+    b = b.to(torch.float8_e4m3fn)
+    sa = 2.0 ** (torch.arange(M, device="cuda") % 5).float()
+    sb = torch.ones(N, device="cuda")
+    sb[::3] = 2.0
+    d = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    plan = migemm.ScaledPlan(M, N, K, a_rs=K, b_cs=K, d_rs=N)
+    assert plan.workspace_size == 0
+    plan.run(a, sa, b, sb, d)
+    torch.cuda.synchronize()
+    for f in range(0, M, 60):
+        want = (total * sb)[None, :] * sa[f:f + 60, None]
+        assert torch.equal(d[f:f + 60], want.bfloat16()), f

@@ -674,9 +674,15 @@ LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_co
   LossChoice c = {};
   const int64_t W = piece < V ? piece : V, sh = (H + 63) / 64, sw = (W + 63) / 64, st = (T + 63) / 64;
   const double t = (double)T, v = (double)V, h = (double)H, w = (double)W;
-  double least_f = 1e300, least_g = 1e300;
+  // A launch holds fewer than 2^32 threads (256 x 256 tiles are taken one after
+  // another).
+  auto fits = [](int tile, int64_t rows, int64_t cols, int splits) {
+    return tile == kLoss256 || (double)loss_tiles(tile, rows, cols) * splits < (1 << 21);
+  };
+  double least_f = 1e301, least_g = 1e301;
   for (int i = 0; i <= kLossRows; ++i) {
     auto logits = [&](LossProduct what, int64_t cols, double bytes) {
+      if (!fits(i, T, cols, 1)) return 1e300;
       if (i < kLossTiles) return cost_of(i, what, T, cols, sh, 1, bytes, cu_count).us;
       // What a compute unit takes in, and the memory.
       const double tiles = (double)loss_tiles(i, T, cols), rounds = tiles > cu_count ? tiles / cu_count : 1.0;
@@ -700,12 +706,13 @@ LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_co
     for (int xs : kSplits) {
       const bool summed = x == kLoss256 || xs > 1 || W < V;
       const double sums = 4 * t * h * xs;
-      if (xs > 1 && (sw < 3 * xs || sums > (512 << 20))) break;
+      if (!fits(x, T, H, xs) || (xs > 1 && (sw < 3 * xs || sums > (512 << 20)))) break;
       const ProductCost dx =
           cost_of(x, kDx, T, H, sw, xs, 2 * (t * w + w * h) + (summed ? sums : 2 * t * h), cu_count);
       const double dx_end = summed ? finish(xs, t * h) : 0;
       for (int y = 0; y < kLossTiles; ++y)
         for (int ys : kSplits) {
+          if (!fits(y, W, H, ys)) break;
           if (ys > 1 && (y == kLoss256 || st < 3 * ys || 4 * w * h * ys > (512 << 20))) break;
           const ProductCost dw =
               cost_of(y, kDw, W, H, st, ys, 2 * (t * w + t * h) + (ys > 1 ? 4 * ys : 2) * w * h, cu_count);

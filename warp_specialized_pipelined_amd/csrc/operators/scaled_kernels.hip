@@ -270,15 +270,35 @@ hipError_t prepare_scaled() {
   return hipSuccess;
 }
 
-hipError_t launch_scaled(const ScaledArgs& s, int variant, int cu_count, hipStream_t stream) {
+hipError_t launch_scaled(const ScaledArgs& all, int variant, int cu_count, hipStream_t stream) {
   const Variant& v = kVariants[variant];
-  const int64_t tiles = tiles_of(v, s.gemm.M, s.gemm.N);
-  const int64_t grid = variant <= kTile192 ? (tiles < cu_count ? tiles : cu_count) : tiles * s.splits;
-  hipLaunchKernelGGL(v.kernel, dim3((uint32_t)grid), dim3(v.threads), v.lds, stream, s);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || s.splits == 1) return e;
-  hipLaunchKernelGGL(v.join, dim3((uint32_t)(tiles * (v.tm / 32) * (v.tn / 32))), dim3(64), 0, stream, s);
-  return hipGetLastError();
+  ScaledArgs s = all;
+  // A launch holds fewer than 2^32 threads: columns in slabs (of whole tiles)
+  // where one tile a workgroup would take more.
+  const int64_t tiles_m = tiles_of(v, all.gemm.M, 1), tiles_n = tiles_of(v, 1, all.gemm.N);
+  int64_t slab = tiles_n;
+  if (variant > kTile192 && tiles_m * tiles_n * s.splits > ((int64_t)1 << 31) / v.threads) {
+    slab = ((int64_t)1 << 31) / v.threads / (tiles_m * s.splits);
+    slab = slab < 1 ? 1 : slab;
+  }
+  for (int64_t first = 0; first < tiles_n; first += slab) {
+    const int64_t col = first * v.tn, left = all.gemm.N - col;
+    s.gemm.N = left < slab * v.tn ? left : slab * v.tn;
+    s.gemm.B = static_cast<const unsigned char*>(all.gemm.B) + col * all.gemm.ldb;
+    s.gemm.b_bytes = (s.gemm.N - 1) * s.gemm.ldb + s.gemm.K;
+    s.gemm.D = static_cast<unsigned short*>(all.gemm.D) + col;
+    s.b_scale = all.b_scale + col;
+    const int64_t tiles = tiles_of(v, s.gemm.M, s.gemm.N);
+    const int64_t grid = variant <= kTile192 ? (tiles < cu_count ? tiles : cu_count) : tiles * s.splits;
+    hipLaunchKernelGGL(v.kernel, dim3((uint32_t)grid), dim3(v.threads), v.lds, stream, s);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && s.splits > 1) {
+      hipLaunchKernelGGL(v.join, dim3((uint32_t)(tiles * (v.tm / 32) * (v.tn / 32))), dim3(64), 0, stream, s);
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace migemm
