@@ -702,32 +702,46 @@ LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_co
   auto finish = [&](int splits, double elements) {
     return launch + 0.15 * splits + (4.0 * splits + 2) * elements / 4.5e6;
   };
+  // Every way that each product can take (a tile, splits; +infinity: none),
+  // and what its sums' end costs.
+  constexpr int kWays = sizeof(kSplits) / sizeof(int);
+  struct Way {
+    double us, items, end;
+  } dx[kLossTiles][kWays], dw[kLossTiles][kWays];
+  for (int i = 0; i < kLossTiles; ++i)
+    for (int k = 0; k < kWays; ++k) {
+      const int n = kSplits[k];
+      const bool summed = i == kLoss256 || n > 1 || W < V;
+      const double sums = 4 * t * h * n, dw_sums = 4 * w * h * n;
+      dx[i][k] = dw[i][k] = {1e300, 0, 0};
+      if (fits(i, T, H, n) && (n == 1 || (sw >= 3 * n && sums <= (512 << 20)))) {
+        const ProductCost p =
+            cost_of(i, kDx, T, H, sw, n, 2 * (t * w + w * h) + (summed ? sums : 2 * t * h), cu_count);
+        dx[i][k] = {p.us, p.items, summed ? finish(n, t * h) : 0};
+      }
+      if (fits(i, W, H, n) && (n == 1 || (i != kLoss256 && st >= 3 * n && dw_sums <= (512 << 20)))) {
+        const ProductCost p =
+            cost_of(i, kDw, W, H, st, n, 2 * (t * w + t * h) + (n > 1 ? dw_sums : 2 * w * h), cu_count);
+        dw[i][k] = {p.us, p.items, n > 1 ? finish(n, w * h) : 0};
+      }
+    }
   for (int x = 0; x < kLossTiles; ++x)
-    for (int xs : kSplits) {
-      const bool summed = x == kLoss256 || xs > 1 || W < V;
-      const double sums = 4 * t * h * xs;
-      if (!fits(x, T, H, xs) || (xs > 1 && (sw < 3 * xs || sums > (512 << 20)))) break;
-      const ProductCost dx =
-          cost_of(x, kDx, T, H, sw, xs, 2 * (t * w + w * h) + (summed ? sums : 2 * t * h), cu_count);
-      const double dx_end = summed ? finish(xs, t * h) : 0;
+    for (int i = 0; i < kWays; ++i) {
+      const Way& p = dx[x][i];
+      if (p.us >= least) continue;
       for (int y = 0; y < kLossTiles; ++y)
-        for (int ys : kSplits) {
-          if (!fits(y, W, H, ys)) break;
-          if (ys > 1 && (y == kLoss256 || st < 3 * ys || 4 * w * h * ys > (512 << 20))) break;
-          const ProductCost dw =
-              cost_of(y, kDw, W, H, st, ys, 2 * (t * w + t * h) + (ys > 1 ? 4 * ys : 2) * w * h, cu_count);
-          const double dw_end = ys > 1 ? finish(ys, w * h) : 0;
-          double both = dx.us + dw.us + launch + dx_end + dw_end;
+        for (int j = 0; j < kWays; ++j) {
+          const Way& q = dw[y][j];
+          double both = p.us + q.us + launch + p.end + q.end;
           if (x == y && x != kLoss256) {
             // Side by side where both fit the chip.
-            both = dx.items + dw.items <= kCost[x].per_cu * (double)cu_count
-                       ? (dx.us > dw.us ? dx.us : dw.us) + 1
-                       : dx.us + dw.us - 2.5;
-            both += dx_end + dw_end - (dx_end > 0 && dw_end > 0 ? launch : 0);
+            both = p.items + q.items <= kCost[x].per_cu * (double)cu_count ? (p.us > q.us ? p.us : q.us) + 1
+                                                                           : p.us + q.us - 2.5;
+            both += p.end + q.end - (p.end > 0 && q.end > 0 ? launch : 0);
           }
           if (both < least) {
             least = both;
-            c.dx = x, c.dx_splits = xs, c.dw = y, c.dw_splits = ys;
+            c.dx = x, c.dx_splits = kSplits[i], c.dw = y, c.dw_splits = kSplits[j];
           }
         }
     }

@@ -2,6 +2,7 @@
 // (include/migemm.h): description checks, plans and run entry points.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -56,14 +57,37 @@ int check_matrix(int64_t rows, int64_t cols, int64_t rs, int es) {
   return MIGEMM_OK;
 }
 
-int check_device(int32_t device, int* cu_count) {
-  int count = 0;
-  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) return MIGEMM_ERR_DEVICE;
-  if (device < 0 || device >= count) return MIGEMM_ERR_DEVICE;
+// What plans need of a device is found out once (the queries take longer than
+// the rest of a plan): its compute units, or a negative status.  `prepare`
+// is the operator's kernels' own preparation, done once a device too.
+constexpr int kMaxDevices = 64;
+int query_device(int32_t device) {
   hipDeviceProp_t prop;
   if (hipGetDeviceProperties(&prop, device) != hipSuccess) return MIGEMM_ERR_DEVICE;
   if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return MIGEMM_ERR_DEVICE;
-  *cu_count = prop.multiProcessorCount;
+  return prop.multiProcessorCount;
+}
+template <class Prepare>
+int check_device(int32_t device, int* cu_count, std::atomic<bool>* prepared, Prepare&& prepare) {
+  static std::atomic<int> found[kMaxDevices];  // 0: not asked yet
+  int count = 0;
+  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) return MIGEMM_ERR_DEVICE;
+  if (device < 0 || device >= count) return MIGEMM_ERR_DEVICE;
+  int cus = device < kMaxDevices ? found[device].load() : 0;
+  if (cus == 0) {
+    cus = query_device(device);
+    if (cus <= 0) return MIGEMM_ERR_DEVICE;
+    if (device < kMaxDevices) found[device].store(cus);
+  }
+  // (Kernel attributes are those of the current device, the one a run checks for.)
+  int current = -1;
+  if (hipGetDevice(&current) != hipSuccess) return MIGEMM_ERR_DEVICE;
+  const bool known = current >= 0 && current < kMaxDevices;
+  if (!known || !prepared[current].load()) {
+    if (prepare() != hipSuccess) return MIGEMM_ERR_DEVICE;
+    if (known) prepared[current].store(true);
+  }
+  *cu_count = cus;
   return MIGEMM_OK;
 }
 
@@ -273,9 +297,9 @@ int gemm_vocab_loss_plan_create(const migemm_vocab_loss_desc* desc, migemm_vocab
   int st = validate_loss(desc);
   if (st != MIGEMM_OK) return st;
   int cus = 0;
-  st = check_device(desc->device, &cus);
+  static std::atomic<bool> prepared[kMaxDevices];
+  st = check_device(desc->device, &cus, prepared, migemm::prepare_loss);
   if (st != MIGEMM_OK) return st;
-  if (migemm::prepare_loss() != hipSuccess) return MIGEMM_ERR_DEVICE;
   migemm_vocab_loss_plan* p = new (std::nothrow) migemm_vocab_loss_plan();
   if (!p) return MIGEMM_ERR_INVALID_ARG;
   p->desc = *desc;
@@ -381,9 +405,9 @@ int gemm_scaled_plan_create(const migemm_scaled_desc* desc, migemm_scaled_plan**
   int st = validate_scaled(desc);
   if (st != MIGEMM_OK) return st;
   int cus = 0;
-  st = check_device(desc->device, &cus);
+  static std::atomic<bool> prepared[kMaxDevices];
+  st = check_device(desc->device, &cus, prepared, migemm::prepare_scaled);
   if (st != MIGEMM_OK) return st;
-  if (migemm::prepare_scaled() != hipSuccess) return MIGEMM_ERR_DEVICE;
   migemm_scaled_plan* p = new (std::nothrow) migemm_scaled_plan();
   if (!p) return MIGEMM_ERR_INVALID_ARG;
   p->desc = *desc;
@@ -434,7 +458,8 @@ int gemm_norm_plan_create(const migemm_norm_desc* desc, migemm_norm_plan** out) 
   int st = validate_norm(desc);
   if (st != MIGEMM_OK) return st;
   int cus = 0;
-  st = check_device(desc->device, &cus);
+  static std::atomic<bool> prepared[kMaxDevices];
+  st = check_device(desc->device, &cus, prepared, [] { return hipSuccess; });
   if (st != MIGEMM_OK) return st;
   migemm_norm_plan* p = new (std::nothrow) migemm_norm_plan();
   if (!p) return MIGEMM_ERR_INVALID_ARG;
