@@ -29,7 +29,11 @@
 // logits with much K take 16 x 32 tiles whose waves split K.
 //
 // Bound: the matrix instructions (one product forward, three backward), or
-// for small ones launches and latency.
+// for small ones launches and latency, or with few tokens reading the weights.
+// Measured: 4096 tokens x 131072 entries x 4096 forward 3.46 ms (1.27
+// PFLOP/s), 8192 tokens forward and backward 26 ms (four products, a tenth of
+// the backward pass's rows left out: 1.25 PFLOP/s); 100 x 50000 x 1000 forward
+// 37 us, of which the tiles take 24 (4.2 TB/s of weights), the join 6.
 #include <hip/hip_runtime.h>
 
 #include <math.h>

