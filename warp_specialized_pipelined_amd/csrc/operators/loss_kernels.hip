@@ -259,17 +259,17 @@ __global__ __launch_bounds__(1024) void loss_join(LossArgs s) {
 
 // The rows that count (0 <= target < V), numbered in order and copied
 // together: x, with what their gradient needs; zeros in dx for the others.
-// from[number] is the row.  Each workgroup takes `rows` consecutive rows, and
-// counts the targets before them itself; the first one also counts them all
-// and finds the largest |dloss|, whose significand (1 .. 2) is the gradients'
-// factor.  A wave copies a row.
+// from[number] is the row.  The first workgroup counts them all and finds the
+// largest |dloss|, whose significand (1 .. 2) is the gradients' factor; each
+// other one takes `rows` consecutive rows, and counts the targets before them
+// itself.  A wave copies a row.
 __global__ __launch_bounds__(1024) void loss_gather_rows(LossArgs s, int64_t rows) {
   __shared__ int totals[16];
   __shared__ float tops[16];
   __shared__ int places[1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // (The last workgroups may have no rows: nothing past T is read either.)
-  const int64_t from_row = (int64_t)blockIdx.x * rows;
+  const int64_t from_row = ((int64_t)blockIdx.x - 1) * rows;
   const int64_t begin = from_row < s.T ? from_row : s.T;
   const int64_t end = begin + rows < s.T ? begin + rows : s.T;
   auto counts = [&](int64_t t) { return t >= 0 && t < s.V; };
@@ -306,6 +306,7 @@ __global__ __launch_bounds__(1024) void loss_gather_rows(LossArgs s, int64_t row
       s.head->count = n;
       s.head->factor = top > 0.0f ? 2.0f * frexpf(top, &exponent) : 1.0f;
     }
+    return;
   }
   int base = 0;
 #pragma unroll 4
@@ -595,11 +596,13 @@ __global__ __launch_bounds__(256, mid_waves(TM, TN, SLOTS)) void loss_products_m
 }
 
 // The sums of one 32 x 32 block of dx (the first dx_blocks workgroups) or dw,
-// added in the order of the splits, scaled and stored.
-template <int TM, int TN>
-__global__ __launch_bounds__(64) void loss_finish(LossArgs s, int dx_blocks) {
+// added up, scaled and stored.  WAVES waves share the splits: each adds its
+// own in order, then the first adds the others' (with 48 splits 4 waves take 6
+// us where one takes 12).
+template <int TM, int TN, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void loss_finish(LossArgs s, int dx_blocks) {
   constexpr int BM = TM / 64, BN = TN / 64;
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
   const bool dx = (int)blockIdx.x < dx_blocks;
   const int at = dx ? blockIdx.x : blockIdx.x - dx_blocks;
   const int64_t M = dx ? s.head->count : s.gemm.M;
@@ -610,13 +613,28 @@ __global__ __launch_bounds__(64) void loss_finish(LossArgs s, int dx_blocks) {
   const MidTile t = TM == kTileM ? MidTile{tile / tiles_n, tile % tiles_n} : mid_tile(tile, tiles_m, tiles_n);
   const int64_t m = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM + 32 * (block / BN) + (lane & 31);
   const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN + 32 * (block % BN);
-  if (m >= M || n0 >= s.H) return;
+  if (m - (lane & 31) >= M || n0 >= s.H) return;  // (the whole workgroup)
   const float factor = s.head->factor;
   MidAccum<1, 1> acc = {};
   const int splits = dx ? s.splits : s.dw_splits;
   const mid_piece* sums = dx ? s.dx_sums : s.dw_sums;
 #pragma unroll 8
-  for (int i = 0; i < splits; ++i) mid_add<BM, BN>(sums, (int64_t)i * tiles_m * tiles_n + tile, acc, wave, block, lane);
+  for (int i = splits * share / WAVES; i < splits * (share + 1) / WAVES; ++i)
+    mid_add<BM, BN>(sums, (int64_t)i * tiles_m * tiles_n + tile, acc, wave, block, lane);
+  if constexpr (WAVES > 1) {
+    __shared__ f32x4 shares[WAVES][4][64];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) shares[share][q][lane] = quarter_of(acc.v[0][0], q);
+    __syncthreads();
+    if (share != 0) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc.v[0][0][4 * q + c] += shares[w][q][lane][c];
+  }
+  if (m >= M) return;
   unsigned short* d = dx ? static_cast<unsigned short*>(s.dx) + (int64_t)s.from[m] * s.dx_rs
                          : static_cast<unsigned short*>(s.gemm.D) + m * s.gemm.ldd;
 #pragma unroll
@@ -638,8 +656,11 @@ constexpr MidKernels mid_kernels() {
 }
 // From kLoss128 on.
 const MidKernels kMid[] = {mid_kernels<128, 128, 2>(), mid_kernels<64, 128, 3>(), mid_kernels<64, 64, 4>()};
-void (*const kFinish[])(LossArgs, int) = {loss_finish<256, 256>, loss_finish<128, 128>, loss_finish<64, 128>,
-                                          loss_finish<64, 64>};
+typedef void (*finish_fn)(LossArgs, int);
+const finish_fn kFinish[][2] = {{loss_finish<256, 256, 1>, loss_finish<256, 256, 4>},
+                                {loss_finish<128, 128, 1>, loss_finish<128, 128, 4>},
+                                {loss_finish<64, 128, 1>, loss_finish<64, 128, 4>},
+                                {loss_finish<64, 64, 1>, loss_finish<64, 64, 4>}};
 
 // What the tiles cost, in microseconds: a K stage of 64 with one tile a
 // compute unit and with two, and a tile besides, by what it makes.
@@ -704,7 +725,7 @@ LossChoice choose_loss(int64_t T, int64_t V, int64_t H, int64_t piece, int cu_co
   constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
   const double launch = 3.5;
   auto finish = [&](int splits, double elements) {
-    return launch + 0.15 * splits + (4.0 * splits + 2) * elements / 4.5e6;
+    return launch + 0.05 * splits + (4.0 * splits + 2) * elements / 4.5e6;
   };
   // Every way that each product can take (a tile, splits; +infinity: none),
   // and what its sums' end costs.
@@ -794,8 +815,8 @@ hipError_t launch_loss_forward(const LossArgs& s, int tile, int cu_count, hipStr
 
 hipError_t launch_loss_rows(const LossArgs& s, hipStream_t stream) {
   int64_t grid = (s.T + 3) / 4;
-  grid = grid < 1 ? 1 : (grid > 256 ? 256 : grid);
-  MIGEMM_LAUNCH(loss_gather_rows, grid, 1024, 0, s, (s.T + grid - 1) / grid);
+  grid = grid < 1 ? 1 : (grid > 255 ? 255 : grid);
+  MIGEMM_LAUNCH(loss_gather_rows, grid + 1, 1024, 0, s, (s.T + grid - 1) / grid);
   return hipSuccess;
 }
 hipError_t launch_loss_gradient(const LossArgs& s, int tile, int cu_count, hipStream_t stream) {
@@ -837,13 +858,15 @@ hipError_t launch_loss_products(const LossArgs& args, const LossChoice& c, bool 
       }
     }
   }
-  if (together && dx_blocks + dw_blocks > 0) {
-    MIGEMM_LAUNCH(kFinish[c.dx], dx_blocks + dw_blocks, 64, 0, s, (int)dx_blocks);
+  auto finish = [&](int tile, int64_t of_dx, int64_t of_dw, int splits) {
+    if (of_dx + of_dw == 0) return hipSuccess;
+    const bool shared = splits >= 8;
+    MIGEMM_LAUNCH(kFinish[tile][shared], of_dx + of_dw, shared ? 256 : 64, 0, s, (int)of_dx);
     return hipSuccess;
-  }
-  if (dw_blocks > 0) MIGEMM_LAUNCH(kFinish[c.dw], dw_blocks, 64, 0, s, 0);
-  if (dx_blocks > 0) MIGEMM_LAUNCH(kFinish[c.dx], dx_blocks, 64, 0, s, (int)dx_blocks);
-  return hipSuccess;
+  };
+  if (together) return finish(c.dx, dx_blocks, dw_blocks, s.splits > s.dw_splits ? s.splits : s.dw_splits);
+  const hipError_t e = finish(c.dw, 0, dw_blocks, s.dw_splits);
+  return e != hipSuccess ? e : finish(c.dx, dx_blocks, 0, s.splits);
 }
 
 }  // namespace migemm
