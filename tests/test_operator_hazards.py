@@ -18,7 +18,7 @@ def kernels(request, tmp_path_factory):
         if any(LDS_LOAD.match(x) for x in lines):
             out[m.group(1)] = lines
     assert out
-    assert request.param != "scaled_kernels" or sum("scaled_mid" in n for n in out) == 4
+    assert request.param != "scaled_kernels" or sum("scaled_mid" in n for n in out) == 5
     return out
 
 

@@ -117,3 +117,28 @@ def test_more_tiles_than_a_launch_has_threads_for():
     for f in range(0, M, 60):
         want = (total * sb)[None, :] * sa[f:f + 60, None]
         assert torch.equal(d[f:f + 60], want.bfloat16()), f
+
+
+# 128 x 128 tiles two a compute unit: K of a few stages and of many, an odd
+# number and an even one, its end inside one; whole and with split sums.
+PAIRS = [(2773, 2191, 552), (1500, 3001, 385), (3000, 2100, 641), (1200, 2000, 9001), (542, 8056, 7030),
+         (2001, 2745, 3100)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", PAIRS)
+def test_two_tiles_a_compute_unit(M, N, K):
+    p = Scaled(M, N, K, seed=M + N + K)
+    p.a[M // 2, K - 1] = float("nan")
+    p.run()
+    torch.cuda.synchronize()
+    nan = torch.isnan(p.d.float())
+    assert nan[M // 2].all() and int(nan.sum()) == N
+    p.a[M // 2, K - 1] = 0.0
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+    first = p.d.clone()
+    p.run()
+    torch.cuda.synchronize()
+    assert torch.equal(p.d, first)

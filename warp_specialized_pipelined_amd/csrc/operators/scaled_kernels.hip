@@ -118,7 +118,7 @@ __global__ __launch_bounds__(64 * W) void scaled_rows(ScaledArgs s) {
 // ranges of K stages.  With one it stores the result; with more each stores
 // its fp32 sums in register order, and scaled_join adds them up.
 template <bool EXACT, int TM, int TN, int SLOTS>
-__global__ __launch_bounds__(256, TM * TN <= 64 * 64 ? 4 : (TM * TN <= 64 * 128 ? 2 : 1)) void scaled_mid(ScaledArgs s) {
+__global__ __launch_bounds__(256, TM * TN <= 64 * 64 ? 4 : (TM * TN <= 64 * 128 || SLOTS == 2 ? 2 : 1)) void scaled_mid(ScaledArgs s) {
   typedef MidGeom<TM, TN, SLOTS> G;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const KernelArgs& a = s.gemm;
@@ -179,7 +179,12 @@ __global__ __launch_bounds__(64) void scaled_join(ScaledArgs s) {
 }
 
 // The kernels a product can take: TM x TN tiles, one a workgroup (256 x 256:
-// one after another).  join: the tile's K may be split.
+// one after another).  join: the tile's K may be split.  128 x 128 comes
+// twice: a ring of four slots, one workgroup a compute unit, hides the loads'
+// latency where there is one tile a unit (424 x 6578 x 7971: 51 us, 58 with
+// two slots); two slots, two workgroups a unit, each loading while the other
+// multiplies, where there are more (1600 x 4000 x 16000: 125 us, 149 with 192
+// rows a tile, 165 with 64 x 128; 2773 x 2191 x 552: 15.0, 25.6 and 18.4).
 struct Variant {
   int tm, tn, threads, lds;
   void (*kernel)(ScaledArgs);
@@ -198,7 +203,7 @@ constexpr Variant mid_variant(int per_cu, double stage1, double stage2, double t
   return {TM, TN, 256, (int)MidGeom<TM, TN, SLOTS>::kLds, scaled_mid<EXACT, TM, TN, SLOTS>,
           EXACT ? nullptr : scaled_join<TM, TN>, per_cu, stage1, stage2, tile};
 }
-enum { kTile256, kTile192, kRowsFirst, kRowsLast = 5, kMidFirst, kMidLast = 8, kExactRows, kExactMid };
+enum { kTile256, kTile192, kRowsFirst, kRowsLast = 5, kMidFirst, kMidLast = 9, kExactRows, kExactMid };
 const Variant kVariants[] = {
     {kTileM, kTileN, kThreads, kPlainLdsBytes, scaled_tile<4>, nullptr, 1, 1.1, 1.1, 7.0},
     {kTileMShort, kTileN, kThreads, kPlainLdsBytes, scaled_tile<3>, nullptr, 1, 0.95, 0.95, 6.0},
@@ -207,8 +212,9 @@ const Variant kVariants[] = {
     rows_variant<1, 2, 2, 8, 1>(2),
     rows_variant<1, 4, 2, 8, 1>(2),
     mid_variant<false, 64, 64, 4>(2, 0.30, 0.48, 1.7),
-    mid_variant<false, 64, 128, 3>(2, 0.39, 0.62, 1.3),
+    mid_variant<false, 64, 128, 3>(2, 0.43, 0.64, 1.3),
     mid_variant<false, 128, 128, 4>(1, 0.52, 0.52, 2.4),
+    mid_variant<false, 128, 128, 2>(2, 0.60, 0.80, 2.0),
     rows_variant<kExactE4M3, 1, 4, 2, 1>(2),
     mid_variant<true, 64, 64, 2>(2, 0, 0, 0),
 };
@@ -231,15 +237,15 @@ double cost_of(const Variant& v, bool rows, int64_t M, int64_t N, int64_t K, int
   double t = full * (stages * v.stage2 + v.tile);
   if (rest > 0) t += stages * (rest <= cus ? v.stage1 : v.stage2) + v.tile;
   t = t > memory ? t : memory;
-  if (splits > 1) t += 3.4 + 2 * items * v.tm * v.tn * 4 / 5.2e6;  // scaled_join, and its sums to memory and back
+  if (splits > 1) t += 4.0 + 2 * items * v.tm * v.tn * 4 / 5.2e6;  // scaled_join, and its sums to memory and back
   return t;
 }
 
 }  // namespace
 
-// The kernel that costs least: the figures are a fit to 450 products of 1 to
+// The kernel that costs least: the figures are a fit to 690 products of 1 to
 // 8192 rows, 64 to 8192 columns and K of 257 to 16384, each timed with every
-// kernel and up to eight splits; what it picks is 2.5% slower than the fastest
+// kernel and up to 16 splits; what it picks is 2.5% slower than the fastest
 // of them on average.
 ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count) {
   // Short sums in exact products: with two K steps at most the time goes into
