@@ -435,7 +435,9 @@ int gemm_norm_run_backward(const migemm_norm_plan* plan, const void* dy, const v
  * once.  From one row to many: the plan chooses among kernels by the sizes,
  * and where it splits K a run needs a workspace for the parts' sums.
  * M, N and K may be 0 (K = 0: d is zero); 256 rows of a, b and d each span
- * less than 2^31 bytes (else UNSUPPORTED). */
+ * less than 2^31 bytes (else UNSUPPORTED).  Strides of whole 128 bytes load
+ * fastest, padded if need be (4000 x 3000 x 5000: 67 us with strides of 5008,
+ * 54 with 5120). */
 typedef struct migemm_scaled_desc {
   int64_t M, N, K;
   int64_t a_rs, b_cs, d_rs;
@@ -470,7 +472,9 @@ int gemm_scaled_run(const migemm_scaled_plan* plan, const void* a, const float* 
  * whose sums are fp32 (with one dloss for every row, as for a mean, the
  * one-hot part is exact).  rows may be 0, vocab and hidden are at
  * least 1; rows and vocab below 2^28, and 256 rows of each matrix span less
- * than 2^31 bytes (else UNSUPPORTED). */
+ * than 2^31 bytes (else UNSUPPORTED).  Strides of whole 128 bytes load fastest
+ * here too (1001 x 32001 x 2000 forward: 150 us with strides of 2000 elements,
+ * 125 with 2048). */
 typedef struct migemm_vocab_loss_desc {
   int64_t rows, vocab, hidden;
   int64_t x_rs, w_rs;
