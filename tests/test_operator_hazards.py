@@ -1,6 +1,6 @@
 """Wait states in front of the LDS-DMA loads of the operators' kernels, and no
 scratch access in their K loops (CPU: compiles to gfx950 assembly, runs
-nothing).  The rules and the checker are test_asm_hazards.py's."""
+nothing).  The rules and their check are test_asm_hazards.py's."""
 import re
 
 import pytest
