@@ -453,6 +453,16 @@ int gemm_scaled_plan_destroy(migemm_scaled_plan* plan);
 /* Bytes of workspace a run needs (256-byte aligned); 0: it may be NULL. */
 size_t gemm_scaled_workspace_size(const migemm_scaled_plan* plan);
 
+/* The kernel a plan has chosen (for tuning and tests). */
+typedef struct migemm_scaled_info {
+  int32_t tile_m, tile_n; /* rows and columns of D a workgroup takes at a time */
+  int32_t lds_stages;     /* 128-byte stages of K in LDS at once; 0: straight to registers */
+  int32_t splits;         /* ranges of K, added up by a second launch if more than 1 */
+  int32_t exact;          /* 1: the codes are multiplied as bf16 */
+  int32_t cu_count;
+} migemm_scaled_info;
+int gemm_scaled_plan_get_info(const migemm_scaled_plan* plan, migemm_scaled_info* info);
+
 /* a_scale is fp32 [M], b_scale fp32 [N], both 16-byte aligned. */
 int gemm_scaled_run(const migemm_scaled_plan* plan, const void* a, const float* a_scale,
                     const void* b, const float* b_scale, void* d, void* workspace, void* stream);

@@ -66,6 +66,13 @@ struct ScaledChoice {
   int64_t workspace_bytes;
 };
 ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count);
+// What a variant's kernel is: its tile, its stages of K in LDS (0: none), and
+// whether it multiplies the codes as bf16.
+struct ScaledKernel {
+  int tile_m, tile_n, lds_stages;
+  bool exact;
+};
+ScaledKernel scaled_kernel(int variant);
 hipError_t prepare_scaled();
 hipError_t launch_scaled(const ScaledArgs& a, int variant, int cu_count, hipStream_t stream);
 

@@ -431,6 +431,13 @@ size_t gemm_scaled_workspace_size(const migemm_scaled_plan* plan) {
   return is_live(plan, kScaled) ? plan->workspace_bytes : 0;
 }
 
+int gemm_scaled_plan_get_info(const migemm_scaled_plan* p, migemm_scaled_info* out) {
+  if (!is_live(p, kScaled) || !out) return MIGEMM_ERR_INVALID_ARG;
+  const migemm::ScaledKernel k = migemm::scaled_kernel(p->variant);
+  *out = {k.tile_m, k.tile_n, k.lds_stages, p->base.splits, k.exact ? 1 : 0, p->cus};
+  return MIGEMM_OK;
+}
+
 int gemm_scaled_run(const migemm_scaled_plan* p, const void* a, const float* a_scale, const void* b,
                     const float* b_scale, void* d, void* workspace, void* stream) {
   if (!is_live(p, kScaled)) return MIGEMM_ERR_INVALID_ARG;

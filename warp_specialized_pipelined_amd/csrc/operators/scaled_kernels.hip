@@ -270,6 +270,12 @@ ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count) {
   return best;
 }
 
+ScaledKernel scaled_kernel(int variant) {
+  const Variant& v = kVariants[variant];
+  const int stages = variant <= kTile192 ? kStages : v.lds / ((v.tm + v.tn) * (int)kStageKBytes);
+  return {v.tm, v.tn, stages, variant >= kExactRows};
+}
+
 hipError_t prepare_scaled() {
   for (const Variant& v : kVariants) {
     if (v.lds == 0) continue;

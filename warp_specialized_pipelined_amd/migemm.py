@@ -45,7 +45,7 @@ EXPORTED = [
     "gemm_norm_desc_validate", "gemm_norm_plan_create", "gemm_norm_plan_destroy",
     "gemm_norm_workspace_size", "gemm_norm_run", "gemm_norm_run_backward",
     "gemm_scaled_desc_validate", "gemm_scaled_plan_create", "gemm_scaled_plan_destroy",
-    "gemm_scaled_workspace_size", "gemm_scaled_run",
+    "gemm_scaled_workspace_size", "gemm_scaled_plan_get_info", "gemm_scaled_run",
     "gemm_vocab_loss_desc_validate", "gemm_vocab_loss_plan_create", "gemm_vocab_loss_plan_destroy",
     "gemm_vocab_loss_workspace_size", "gemm_vocab_loss_run", "gemm_vocab_loss_run_backward",
 ]
@@ -109,6 +109,10 @@ class migemm_scaled_desc(ctypes.Structure):
         ("a_rs", ctypes.c_int64), ("b_cs", ctypes.c_int64), ("d_rs", ctypes.c_int64),
         ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
+
+
+class migemm_scaled_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tile_m", "tile_n", "lds_stages", "splits", "exact", "cu_count")]
 
 
 class migemm_vocab_loss_desc(ctypes.Structure):
@@ -177,7 +181,7 @@ def load(path: str | None = None):
     lib.gemm_norm_run.restype = i32
     lib.gemm_norm_run_backward.argtypes = [vp] * 10
     lib.gemm_norm_run_backward.restype = i32
-    _declare_plan_calls(lib, "scaled", migemm_scaled_desc)
+    _declare_plan_calls(lib, "scaled", migemm_scaled_desc, migemm_scaled_info)
     lib.gemm_scaled_run.argtypes = [vp] * 8
     lib.gemm_scaled_run.restype = i32
     _declare_plan_calls(lib, "vocab_loss", migemm_vocab_loss_desc)
@@ -191,13 +195,16 @@ def load(path: str | None = None):
     return lib
 
 
-def _declare_plan_calls(lib, kind, desc):
+def _declare_plan_calls(lib, kind, desc, info=None):
     """The calls every operator's plan has."""
     vp, i32, P = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER
-    for name, args, res in (("desc_validate", [P(desc)], i32),
-                            ("plan_create", [P(desc), P(vp)], i32),
-                            ("plan_destroy", [vp], i32),
-                            ("workspace_size", [vp], ctypes.c_size_t)):
+    calls = [("desc_validate", [P(desc)], i32),
+             ("plan_create", [P(desc), P(vp)], i32),
+             ("plan_destroy", [vp], i32),
+             ("workspace_size", [vp], ctypes.c_size_t)]
+    if info is not None:
+        calls.append(("plan_get_info", [vp, P(info)], i32))
+    for name, args, res in calls:
         f = getattr(lib, f"gemm_{kind}_{name}")
         f.argtypes, f.restype = args, res
 
@@ -423,6 +430,7 @@ class _OperatorPlan:
     """Owns an operator's plan handle; destroys it when garbage-collected."""
 
     kind = ""
+    info_type = None
 
     def __init__(self, desc):
         self.desc = desc
@@ -435,6 +443,15 @@ class _OperatorPlan:
     @property
     def workspace_size(self) -> int:
         return int(getattr(load(), f"gemm_{self.kind}_workspace_size")(self.handle))
+
+    @property
+    def info(self):
+        """The kernels the plan has chosen."""
+        info = self.info_type()
+        st = getattr(load(), f"gemm_{self.kind}_plan_get_info")(self.handle, ctypes.byref(info))
+        if st != MIGEMM_OK:
+            raise MigemmError(st, f"gemm_{self.kind}_plan_get_info")
+        return info
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -470,6 +487,7 @@ class ScaledPlan(_OperatorPlan):
     b (N x K e4m3, a scale per row); row strides in elements."""
 
     kind = "scaled"
+    info_type = migemm_scaled_info
 
     def __init__(self, M, N, K, *, a_rs, b_cs, d_rs, device=0):
         super().__init__(migemm_scaled_desc(M, N, K, a_rs, b_cs, d_rs, device, 0))
