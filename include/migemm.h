@@ -503,6 +503,21 @@ int gemm_vocab_loss_plan_destroy(migemm_vocab_loss_plan* plan);
  * that count, one piece of g (up to 512 MiB) and fp32 sums of dx and dw. */
 size_t gemm_vocab_loss_workspace_size(const migemm_vocab_loss_plan* plan);
 
+/* The kernels a plan has chosen (for tuning and tests): the tiles (rows x
+ * columns) of the logits forward and backward and of the backward pass's two
+ * products, the ranges of K that those split into, and the vocabulary entries
+ * that the backward pass takes at a time.  0 without a backward pass. */
+typedef struct migemm_vocab_loss_info {
+  int32_t forward_tile_m, forward_tile_n;
+  int32_t gradient_tile_m, gradient_tile_n;
+  int32_t dx_tile_m, dx_tile_n, dx_splits;
+  int32_t dw_tile_m, dw_tile_n, dw_splits;
+  int32_t cu_count;
+  int32_t pieces;
+  int64_t piece;
+} migemm_vocab_loss_info;
+int gemm_vocab_loss_plan_get_info(const migemm_vocab_loss_plan* plan, migemm_vocab_loss_info* info);
+
 /* target is int64 [rows]; loss and lse are fp32 [rows]. */
 int gemm_vocab_loss_run(const migemm_vocab_loss_plan* plan, const void* x, const void* w,
                         const int64_t* target, float* loss, float* lse, void* workspace,

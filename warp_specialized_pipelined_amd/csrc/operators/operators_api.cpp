@@ -314,6 +314,22 @@ size_t gemm_vocab_loss_workspace_size(const migemm_vocab_loss_plan* plan) {
   return is_live(plan, kVocabLoss) ? plan->workspace_bytes : 0;
 }
 
+int gemm_vocab_loss_plan_get_info(const migemm_vocab_loss_plan* p, migemm_vocab_loss_info* out) {
+  if (!is_live(p, kVocabLoss) || !out) return MIGEMM_ERR_INVALID_ARG;
+  const migemm::LossChoice& c = p->choice;
+  const auto m = [](int tile) { return (int32_t)migemm::kLossTileM[tile]; };
+  const auto n = [](int tile) { return (int32_t)migemm::kLossTileN[tile]; };
+  *out = {m(c.forward), n(c.forward)};
+  out->cu_count = p->cus;
+  if (p->desc.dx_rs == 0) return MIGEMM_OK;
+  out->gradient_tile_m = m(c.gradient), out->gradient_tile_n = n(c.gradient);
+  out->dx_tile_m = m(c.dx), out->dx_tile_n = n(c.dx), out->dx_splits = c.dx_splits;
+  out->dw_tile_m = m(c.dw), out->dw_tile_n = n(c.dw), out->dw_splits = c.dw_splits;
+  out->pieces = (int32_t)((p->desc.vocab + p->piece - 1) / p->piece);
+  out->piece = p->piece;
+  return MIGEMM_OK;
+}
+
 int gemm_vocab_loss_run(const migemm_vocab_loss_plan* p, const void* x, const void* w,
                         const int64_t* target, float* loss, float* lse, void* workspace,
                         void* stream) {

@@ -47,7 +47,7 @@ EXPORTED = [
     "gemm_scaled_desc_validate", "gemm_scaled_plan_create", "gemm_scaled_plan_destroy",
     "gemm_scaled_workspace_size", "gemm_scaled_plan_get_info", "gemm_scaled_run",
     "gemm_vocab_loss_desc_validate", "gemm_vocab_loss_plan_create", "gemm_vocab_loss_plan_destroy",
-    "gemm_vocab_loss_workspace_size", "gemm_vocab_loss_run", "gemm_vocab_loss_run_backward",
+    "gemm_vocab_loss_workspace_size", "gemm_vocab_loss_plan_get_info", "gemm_vocab_loss_run", "gemm_vocab_loss_run_backward",
 ]
 
 
@@ -124,6 +124,13 @@ class migemm_vocab_loss_desc(ctypes.Structure):
     ]
 
 
+class migemm_vocab_loss_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "forward_tile_m", "forward_tile_n", "gradient_tile_m", "gradient_tile_n",
+        "dx_tile_m", "dx_tile_n", "dx_splits", "dw_tile_m", "dw_tile_n", "dw_splits",
+        "cu_count", "pieces")] + [("piece", ctypes.c_int64)]
+
+
 class MigemmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -184,7 +191,7 @@ def load(path: str | None = None):
     _declare_plan_calls(lib, "scaled", migemm_scaled_desc, migemm_scaled_info)
     lib.gemm_scaled_run.argtypes = [vp] * 8
     lib.gemm_scaled_run.restype = i32
-    _declare_plan_calls(lib, "vocab_loss", migemm_vocab_loss_desc)
+    _declare_plan_calls(lib, "vocab_loss", migemm_vocab_loss_desc, migemm_vocab_loss_info)
     lib.gemm_vocab_loss_run.argtypes = [vp] * 8
     lib.gemm_vocab_loss_run.restype = i32
     lib.gemm_vocab_loss_run_backward.argtypes = [vp] * 10
@@ -502,6 +509,7 @@ class VocabLossPlan(_OperatorPlan):
     a backward pass."""
 
     kind = "vocab_loss"
+    info_type = migemm_vocab_loss_info
 
     def __init__(self, rows, vocab, hidden, *, x_rs, w_rs, dx_rs=0, dw_rs=0, device=0):
         super().__init__(migemm_vocab_loss_desc(rows, vocab, hidden, x_rs, w_rs, dx_rs, dw_rs, device, 0))
