@@ -413,6 +413,17 @@ int gemm_norm_plan_destroy(migemm_norm_plan* plan);
  * plan without a backward pass. */
 size_t gemm_norm_workspace_size(const migemm_norm_plan* plan);
 
+/* The kernels a plan has chosen (for tuning and tests): the waves that share a
+ * row and the 16-byte vectors of it that each lane holds, and the workgroups
+ * that walk the rows backward (0 without a backward pass). */
+typedef struct migemm_norm_info {
+  int32_t forward_waves, forward_vectors;
+  int32_t backward_waves, backward_vectors;
+  int32_t backward_workgroups;
+  int32_t cu_count;
+} migemm_norm_info;
+int gemm_norm_plan_get_info(const migemm_norm_plan* plan, migemm_norm_info* info);
+
 /* r and h are given exactly when the plan has a residual, scale (fp32 [rows])
  * exactly when y is e4m3; rstd is fp32 [rows], weight bf16 [cols], 16-byte
  * aligned.  h may be x or r itself (same strides), and a bf16 y may be x. */

@@ -35,6 +35,7 @@ struct migemm_vocab_loss_plan {
 
 struct migemm_norm_plan {
   migemm_norm_desc desc;
+  int cus;
   int64_t partial_rows;
   size_t workspace_bytes;
 };
@@ -487,6 +488,7 @@ int gemm_norm_plan_create(const migemm_norm_desc* desc, migemm_norm_plan** out) 
   migemm_norm_plan* p = new (std::nothrow) migemm_norm_plan();
   if (!p) return MIGEMM_ERR_INVALID_ARG;
   p->desc = *desc;
+  p->cus = cus;
   if (norm_backward(*desc)) {
     p->partial_rows = migemm::norm_partial_rows(desc->rows, desc->cols, cus);
     p->workspace_bytes = (size_t)(p->partial_rows * desc->cols * 4);
@@ -498,6 +500,18 @@ int gemm_norm_plan_destroy(migemm_norm_plan* plan) { return destroy(plan, kNorm)
 
 size_t gemm_norm_workspace_size(const migemm_norm_plan* plan) {
   return is_live(plan, kNorm) ? plan->workspace_bytes : 0;
+}
+
+int gemm_norm_plan_get_info(const migemm_norm_plan* p, migemm_norm_info* out) {
+  if (!is_live(p, kNorm) || !out) return MIGEMM_ERR_INVALID_ARG;
+  const migemm::NormShape f = migemm::norm_forward_shape(p->desc.rows, p->desc.cols);
+  *out = {f.waves, f.vectors};
+  out->cu_count = p->cus;
+  if (!norm_backward(p->desc)) return MIGEMM_OK;
+  const migemm::NormShape b = migemm::norm_backward_shape(p->desc.rows, p->desc.cols);
+  out->backward_waves = b.waves, out->backward_vectors = b.vectors;
+  out->backward_workgroups = (int32_t)p->partial_rows;
+  return MIGEMM_OK;
 }
 
 int gemm_norm_run(const migemm_norm_plan* p, const void* x, const void* r, const void* weight,

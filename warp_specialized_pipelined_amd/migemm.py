@@ -43,7 +43,7 @@ EXPORTED = [
     "gemm_plan_workspace_size", "gemm_workspace_init", "gemm_run", "gemm_run_with_tile_consumer",
     "gemm_run_no_alloc", "gemm_debug_read", "gemm_status_string",
     "gemm_norm_desc_validate", "gemm_norm_plan_create", "gemm_norm_plan_destroy",
-    "gemm_norm_workspace_size", "gemm_norm_run", "gemm_norm_run_backward",
+    "gemm_norm_workspace_size", "gemm_norm_plan_get_info", "gemm_norm_run", "gemm_norm_run_backward",
     "gemm_scaled_desc_validate", "gemm_scaled_plan_create", "gemm_scaled_plan_destroy",
     "gemm_scaled_workspace_size", "gemm_scaled_plan_get_info", "gemm_scaled_run",
     "gemm_vocab_loss_desc_validate", "gemm_vocab_loss_plan_create", "gemm_vocab_loss_plan_destroy",
@@ -101,6 +101,12 @@ class migemm_norm_desc(ctypes.Structure):
         ("eps", ctypes.c_float), ("y_type", ctypes.c_int32),
         ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
+
+
+class migemm_norm_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "forward_waves", "forward_vectors", "backward_waves", "backward_vectors",
+        "backward_workgroups", "cu_count")]
 
 
 class migemm_scaled_desc(ctypes.Structure):
@@ -183,7 +189,7 @@ def load(path: str | None = None):
     lib.gemm_run_no_alloc.restype = i32
     lib.gemm_debug_read.argtypes = [vp, vp, vp, P(migemm_debug_info)]
     lib.gemm_debug_read.restype = i32
-    _declare_plan_calls(lib, "norm", migemm_norm_desc)
+    _declare_plan_calls(lib, "norm", migemm_norm_desc, migemm_norm_info)
     lib.gemm_norm_run.argtypes = [vp] * 9
     lib.gemm_norm_run.restype = i32
     lib.gemm_norm_run_backward.argtypes = [vp] * 10
@@ -202,16 +208,14 @@ def load(path: str | None = None):
     return lib
 
 
-def _declare_plan_calls(lib, kind, desc, info=None):
+def _declare_plan_calls(lib, kind, desc, info):
     """The calls every operator's plan has."""
     vp, i32, P = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER
-    calls = [("desc_validate", [P(desc)], i32),
-             ("plan_create", [P(desc), P(vp)], i32),
-             ("plan_destroy", [vp], i32),
-             ("workspace_size", [vp], ctypes.c_size_t)]
-    if info is not None:
-        calls.append(("plan_get_info", [vp, P(info)], i32))
-    for name, args, res in calls:
+    for name, args, res in (("desc_validate", [P(desc)], i32),
+                            ("plan_create", [P(desc), P(vp)], i32),
+                            ("plan_destroy", [vp], i32),
+                            ("plan_get_info", [vp, P(info)], i32),
+                            ("workspace_size", [vp], ctypes.c_size_t)):
         f = getattr(lib, f"gemm_{kind}_{name}")
         f.argtypes, f.restype = args, res
 
@@ -476,6 +480,7 @@ class NormPlan(_OperatorPlan):
     and dx_rs (and dh_rs): with a backward pass."""
 
     kind = "norm"
+    info_type = migemm_norm_info
 
     def __init__(self, rows, cols, eps, y_type=MIGEMM_BF16, *, x_rs, y_rs, r_rs=0, h_rs=0, dy_rs=0,
                  dx_rs=0, dh_rs=0, device=0):
