@@ -13,6 +13,7 @@
 #include "../../include/migemm.h"
 #include "kernel/params.hpp"
 #include "launch.h"
+#include "on_device.hpp"
 
 using migemm::KernelArgs;
 using migemm::KernelSelect;
@@ -400,13 +401,14 @@ int gemm_plan_create(const migemm_desc* desc, migemm_plan** out) {
                              migemm::kTraceWords * sizeof(uint64_t);
   }
 
-  hipError_t e = migemm::prepare_kernel(p->sel);
-  if (e == hipSuccess && (desc->flags & MIGEMM_F_TILE_CONSUMER)) {
+  const bool prepared = migemm::prepare_on(p->device, [&] {
+    const hipError_t e = migemm::prepare_kernel(p->sel);
+    if (e != hipSuccess || !(desc->flags & MIGEMM_F_TILE_CONSUMER)) return e;
     KernelSelect s = p->sel;
     s.consumer = true;
-    e = migemm::prepare_kernel(s);
-  }
-  if (e != hipSuccess) {
+    return migemm::prepare_kernel(s);
+  });
+  if (!prepared) {
     delete p;
     return MIGEMM_ERR_DEVICE;
   }

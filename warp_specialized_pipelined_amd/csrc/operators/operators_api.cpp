@@ -10,6 +10,7 @@
 #include <unordered_map>
 
 #include "../../../include/migemm.h"
+#include "../on_device.hpp"
 #include "operators.h"
 
 struct migemm_scaled_plan {
@@ -80,13 +81,10 @@ int check_device(int32_t device, int* cu_count, std::atomic<bool>* prepared, Pre
     if (cus <= 0) return MIGEMM_ERR_DEVICE;
     if (device < kMaxDevices) found[device].store(cus);
   }
-  // (Kernel attributes are those of the current device, the one a run checks for.)
-  int current = -1;
-  if (hipGetDevice(&current) != hipSuccess) return MIGEMM_ERR_DEVICE;
-  const bool known = current >= 0 && current < kMaxDevices;
-  if (!known || !prepared[current].load()) {
-    if (prepare() != hipSuccess) return MIGEMM_ERR_DEVICE;
-    if (known) prepared[current].store(true);
+  const bool known = device < kMaxDevices;
+  if (!known || !prepared[device].load()) {
+    if (!migemm::prepare_on(device, prepare)) return MIGEMM_ERR_DEVICE;
+    if (known) prepared[device].store(true);
   }
   *cu_count = cus;
   return MIGEMM_OK;
