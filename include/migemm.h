@@ -516,7 +516,11 @@ int gemm_vocab_loss_plan_create(const migemm_vocab_loss_desc* desc, migemm_vocab
 int gemm_vocab_loss_plan_destroy(migemm_vocab_loss_plan* plan);
 /* Bytes of workspace either run needs (256-byte aligned).  Forward: 8 bytes a
  * row (of up to 16384) and 16 to 128 vocabulary entries.  Backward: the rows
- * that count, one piece of g (up to 512 MiB) and fp32 sums of dx and dw. */
+ * that count, copied together; one piece of g, 2 bytes a row and entry of as
+ * many entries as fit 512 MiB, but 1024 at least, and 64 more a row; fp32 sums
+ * of dx, 4 bytes a row and hidden unit, unless one workgroup finishes each of
+ * its tiles; and where K is split, that many of dx or of the piece's dw, up to
+ * 512 MiB each (all of them in whole tiles). */
 size_t gemm_vocab_loss_workspace_size(const migemm_vocab_loss_plan* plan);
 
 /* The kernels a plan has chosen (for tuning and tests): the tiles (rows x

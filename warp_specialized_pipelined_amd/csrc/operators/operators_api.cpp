@@ -233,16 +233,20 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // Rows of the forward pass a launch takes: their pairs of the whole
 // vocabulary are the workspace (at 131072 entries 128 MiB).
 constexpr int64_t kLossChunk = 16384;
-// The most a piece of g takes.
+// The most a piece of g takes, the padding of its rows aside -- unless that is
+// less than kPieceLeast entries: adding a piece's dx to the fp32 sums moves 8
+// bytes a row and hidden unit, which takes the time of a product of about that
+// many entries, and smaller pieces would spend more on it than on the product.
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;
+constexpr int64_t kPieceLeast = 1024;
 
 void lay_out_loss(migemm_vocab_loss_plan* p) {
   const migemm_vocab_loss_desc& d = p->desc;
   const int64_t T = d.rows, V = d.vocab, H = d.hidden;
   p->chunk = T < kLossChunk ? T : kLossChunk;
-  // Pieces of g within kPieceBytes, of equal width.
+  // Pieces of equal width.
   int64_t most = kPieceBytes / 2 / up(T > 0 ? T : 1, 256) / 256 * 256;
-  most = most < 1024 ? 1024 : (most > (1 << 20) ? 1 << 20 : most);
+  most = most < kPieceLeast ? kPieceLeast : (most > (1 << 20) ? 1 << 20 : most);
   const int64_t pieces = (V + most - 1) / most;
   p->piece = up((V + pieces - 1) / pieces, 256);
   p->choice = migemm::choose_loss(T, V, H, p->piece, p->cus);
