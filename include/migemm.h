@@ -493,10 +493,12 @@ int gemm_scaled_run(const migemm_scaled_plan* plan, const void* a, const float* 
  *   dx = bf16(g w),   dw = bf16(g^T x)
  * where a row whose target is not in [0, vocab) has g = 0 exactly, whatever
  * x and dloss hold there: its dx is 0, and it adds nothing to dw.  lse is
- * written for every row.  g, over the significand of the largest |dloss| of
- * the rows that count, is rounded to bf16 on its way into the two products,
- * whose sums are fp32 (with one dloss for every row, as for a mean, the
- * one-hot part is exact).  rows may be 0, vocab and hidden are at
+ * written for every row.  Logits, sums and exponentials are fp32.  g, over the
+ * significand of the largest |dloss| of the rows that count, is rounded to bf16
+ * on its way into the two products, whose sums are fp32: one rounding of each
+ * entry of g, 2^-8 at most, beside that of dx and dw themselves (with one dloss
+ * for every row, as for a mean, the one-hot part is exact before the target's
+ * probability is added to it).  rows may be 0, vocab and hidden are at
  * least 1; rows and vocab below 2^28, and 256 rows of each matrix span less
  * than 2^31 bytes (else UNSUPPORTED).  Strides of whole 128 bytes load fastest
  * here too (1001 x 32001 x 2000 forward: 150 us with strides of 2000 elements,

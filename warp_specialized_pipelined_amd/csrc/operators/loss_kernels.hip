@@ -16,12 +16,16 @@
 // logits are formed again, g of the piece is stored as bf16, and two products
 // read it: dw of the piece, complete, and the piece's share of dx, added up
 // in fp32.  g is the one quantity rounded to bf16 in between: the matrix
-// instructions take bf16 pairs.  It is divided by the significand of the
-// largest |dloss|, and the products are multiplied by it in fp32: where dloss
-// is the same in every row, as for a mean, the one-hot part, which makes up
-// nearly all of g, is then a power of two, and what is rounded (half a step,
-// 2^-9 on average, of each exp(logits - lse)) is far below the rounding of the
-// outputs.
+// instructions take bf16 pairs, and g in two bf16 parts would take both
+// products twice.  That adds one rounding, independent from entry to entry, to
+// the outputs' own: the gradients' error against 64 bits is 0.0022 to 0.0023 of
+// their norm, the outputs' rounding alone 0.0017 (1001 tokens x 32001 entries x
+// 2000).  g is divided by the significand of the largest |dloss|, and the
+// products are multiplied by it in fp32: where dloss is the same in every row,
+// as for a mean, the one-hot part is then a power of two, and what is rounded is
+// the sum of it and the target's probability: 0.0017 where that is small (random
+// targets), 0.0018 with targets drawn from the model's own probabilities, 0.0020
+// where those are 0.13 on average.
 //
 // The tiles are 256 x 256 with the GEMM's K loop, or 128 or 64 rows and columns
 // (midtile.hpp) where those are too few or too large; in the backward pass
