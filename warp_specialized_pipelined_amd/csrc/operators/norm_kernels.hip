@@ -14,12 +14,12 @@
 //   dx = rstd (g w - n mean(g w n)) + dh,   dweight = sum over rows of g n
 //
 // Bound: memory (4 to 14 bytes an element).  A row is read once, 16 bytes a
-// lane, and stays in registers between the reduction and the output; one wave
-// a row up to 1024 columns, else 4 or 16, so that a lane holds at most 32
-// values.  Measured: 8192 x 8192 to e4m3 rows 83 us (5.7 TB/s); 4000 x 5000
-// without a residual 15 us (5.3 TB/s); 8192 x 4096 forward 46 us and backward
-// 47 us (5.8 and 5.7 TB/s) and 5 us for the column sums; one row of 8192
-// 3.2 us (with 4 waves instead of 16: 3.9; a row of 1000 to bf16: 2.4).
+// lane, and stays in registers between the reduction and the output.  Measured:
+// 8192 x 8192 to e4m3 rows 82 us (5.7 TB/s); 4000 x 5000 without a residual 15
+// us where its 80 MB are still in the last-level cache, 20 from memory (4.1
+// TB/s); 8192 x 4096 forward 46 us and backward 47 us (5.8 and 5.7 TB/s) and 5
+// us for the column sums; one row of 8192 3.2 us (with 4 waves instead of 16:
+// 3.9; a row of 1000 to bf16: 2.4).
 #include <hip/hip_runtime.h>
 
 #include "../kernel/gfx950.hpp"
@@ -355,35 +355,33 @@ norm_fn backward_pick(int nv, bool res) {
                  : (nv == 2 ? norm_backward<WAVES, 2, false> : norm_backward<WAVES, 4, false>);
 }
 
+}  // namespace
+
 // The fewest waves (1, 4, 16) whose lanes hold the row in `most` vectors, and
-// the vectors that takes.
-NormShape shape_for(int64_t cols, int most) {
+// the vectors that takes.  Few rows: one vector a lane where 16 waves allow, for
+// a row's latency counts (one wave up to 512 columns, four up to 2048).  Many:
+// up to four (one wave up to 2048 columns, four up to 8192), which leaves more
+// rows in flight: 8192 x 1100 forward and backward 45 us with one wave a row, 66
+// with four, 4096 x 1100 29 and 38 (8192 x 2048 53 and 56; at 1000 x 2048 four
+// waves are 2 us faster, 14 and 16).
+NormShape norm_shape(int64_t rows, int64_t cols) {
+  const int most = rows <= 256 ? 1 : 4;
   int waves = 1;
   while (waves < 16 && (int64_t)waves * 512 * most < cols) waves *= 4;
   const int64_t v = (cols + waves * 512 - 1) / (waves * 512);
   return {waves, v <= 1 ? 1 : (v <= 2 ? 2 : 4)};
 }
 
-}  // namespace
-
-// With few rows a row's latency counts: one vector a lane where waves allow.
-NormShape norm_forward_shape(int64_t rows, int64_t cols) {
-  return shape_for(cols, rows <= 256 ? 1 : (cols <= 1024 ? 2 : 4));
-}
-NormShape norm_backward_shape(int64_t rows, int64_t cols) {
-  return shape_for(cols, rows <= 256 ? 1 : (cols <= 1024 ? 2 : 4));
-}
-
 // A second kernel costs about as much as three rows one after another.
 int64_t norm_partial_rows(int64_t rows, int64_t cols, int cu_count) {
-  const int at_once = rows_of(norm_backward_shape(rows, cols).waves);
+  const int at_once = rows_of(norm_shape(rows, cols).waves);
   if (rows <= 3 * at_once) return rows > 0 ? 1 : 0;
   const int64_t groups = (rows + at_once - 1) / at_once, most = (int64_t)cu_count * 2;
   return groups < most ? groups : most;
 }
 
 hipError_t launch_norm_forward(const NormArgs& a, bool e4m3, hipStream_t stream) {
-  const NormShape s = norm_forward_shape(a.rows, a.cols);
+  const NormShape s = norm_shape(a.rows, a.cols);
   const bool res = a.r != nullptr;
   const norm_fn f = s.waves == 1 ? forward_pick<1>(s.vectors, res, e4m3)
                                  : (s.waves == 4 ? forward_pick<4>(s.vectors, res, e4m3)
@@ -395,7 +393,7 @@ hipError_t launch_norm_forward(const NormArgs& a, bool e4m3, hipStream_t stream)
 }
 
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream) {
-  const NormShape s = norm_backward_shape(a.rows, a.cols);
+  const NormShape s = norm_shape(a.rows, a.cols);
   const bool res = a.dh != nullptr;
   if (a.partial_rows > 0) {
     const norm_fn f = s.waves == 1 ? backward_pick<1>(s.vectors, res)

@@ -38,8 +38,7 @@ constexpr int64_t kNormMaxCols = 16 * 64 * 4 * 8;
 struct NormShape {
   int waves, vectors;
 };
-NormShape norm_forward_shape(int64_t rows, int64_t cols);
-NormShape norm_backward_shape(int64_t rows, int64_t cols);
+NormShape norm_shape(int64_t rows, int64_t cols);
 // Rows of partial column sums the backward pass leaves in its workspace.
 int64_t norm_partial_rows(int64_t rows, int64_t cols, int cu_count);
 

@@ -506,13 +506,9 @@ size_t gemm_norm_workspace_size(const migemm_norm_plan* plan) {
 
 int gemm_norm_plan_get_info(const migemm_norm_plan* p, migemm_norm_info* out) {
   if (!is_live(p, kNorm) || !out) return MIGEMM_ERR_INVALID_ARG;
-  const migemm::NormShape f = migemm::norm_forward_shape(p->desc.rows, p->desc.cols);
-  *out = {f.waves, f.vectors};
-  out->cu_count = p->cus;
-  if (!norm_backward(p->desc)) return MIGEMM_OK;
-  const migemm::NormShape b = migemm::norm_backward_shape(p->desc.rows, p->desc.cols);
-  out->backward_waves = b.waves, out->backward_vectors = b.vectors;
-  out->backward_workgroups = (int32_t)p->partial_rows;
+  const migemm::NormShape f = migemm::norm_shape(p->desc.rows, p->desc.cols);
+  const bool back = norm_backward(p->desc);
+  *out = {f.waves, f.vectors, back ? f.waves : 0, back ? f.vectors : 0, (int32_t)p->partial_rows, p->cus};
   return MIGEMM_OK;
 }
 
