@@ -50,7 +50,9 @@ extern "C" {
 /* Element types (the pages keep ElementA/B/C/D separate). */
 typedef enum migemm_dtype {
   MIGEMM_BF16 = 1,
-  MIGEMM_FP8_E4M3 = 2
+  MIGEMM_FP8_E4M3 = 2,
+  MIGEMM_INT8 = 3, /* where a description of an operator names it */
+  MIGEMM_FP32 = 4  /* likewise */
 } migemm_dtype;
 
 typedef enum migemm_status {
@@ -552,6 +554,210 @@ int gemm_vocab_loss_run(const migemm_vocab_loss_plan* plan, const void* x, const
 int gemm_vocab_loss_run_backward(const migemm_vocab_loss_plan* plan, const void* x, const void* w,
                                  const int64_t* target, const float* lse, const float* dloss,
                                  void* dx, void* dw, void* workspace, void* stream);
+
+/* The product of int8 rows, each with its scale, and int8 weights with a scale
+ * per output channel, with a bias per channel or none:
+ *   d[m][n] = bf16(a_scale[m] * b_scale[n] * sum over k of a[m][k] b[n][k] + bias[n])
+ * a is M x K and b N x K int8 (both K-contiguous, as the scaled product's), any
+ * codes from -128 to 127; d is M x N bf16.  The sum is int32 and exact, then
+ * rounded to fp32 (2^-24 of it); scales and bias are fp32, and the result is
+ * rounded to bf16 once.  K is at most 131071 (more: UNSUPPORTED), so that no
+ * sum leaves int32.  Otherwise sizes, strides and the workspace are as the
+ * scaled product's. */
+typedef struct migemm_int8_desc {
+  int64_t M, N, K;
+  int64_t a_rs, b_cs, d_rs;
+  int32_t device;
+  int32_t reserved; /* must be 0 */
+} migemm_int8_desc;
+
+typedef struct migemm_int8_plan migemm_int8_plan; /* opaque, host memory only */
+
+int gemm_int8_desc_validate(const migemm_int8_desc* desc);
+int gemm_int8_plan_create(const migemm_int8_desc* desc, migemm_int8_plan** out);
+int gemm_int8_plan_destroy(migemm_int8_plan* plan);
+/* Bytes of workspace a run needs (256-byte aligned); 0: it may be NULL. */
+size_t gemm_int8_workspace_size(const migemm_int8_plan* plan);
+
+/* The kernel a plan has chosen (for tuning and tests). */
+typedef struct migemm_int8_info {
+  int32_t tile_m, tile_n; /* rows and columns of D a workgroup takes at a time */
+  int32_t lds_stages;     /* 128-byte stages of K in LDS at once; 0: straight to registers */
+  int32_t splits;         /* ranges of K, added up by a second launch if more than 1 */
+  int32_t cu_count;
+} migemm_int8_info;
+int gemm_int8_plan_get_info(const migemm_int8_plan* plan, migemm_int8_info* info);
+
+/* a_scale is fp32 [M], b_scale and bias fp32 [N], all 16-byte aligned; bias may
+ * be NULL. */
+int gemm_int8_run(const migemm_int8_plan* plan, const void* a, const float* a_scale, const void* b,
+                  const float* b_scale, const float* bias, void* d, void* workspace, void* stream);
+
+/* bf16 rows to 8 bits with a scale each: the rows that gemm_int8_run (q_type
+ * MIGEMM_INT8, top = 127) and gemm_scaled_run (MIGEMM_FP8_E4M3, top = 448) take.
+ *   scale = max |x| / top  (fp32),   q = x * top / max |x|
+ * q rounded to the nearest code, ties to even, as if from the exact quotient.
+ * A row of zeros gets scale 0 and codes 0; a row with an infinity or a NaN gets
+ * scale NaN and codes 0, so that its products are NaN.  cols is 1 .. 32768
+ * (above: UNSUPPORTED); rows may be 0. */
+typedef struct migemm_quantize_desc {
+  int64_t rows, cols;
+  int64_t x_rs, q_rs; /* x: bf16; q: q_type */
+  int32_t q_type;     /* MIGEMM_INT8 or MIGEMM_FP8_E4M3 */
+  int32_t device;
+  int64_t reserved;   /* must be 0 */
+} migemm_quantize_desc;
+
+typedef struct migemm_quantize_plan migemm_quantize_plan; /* opaque, host memory only */
+
+int gemm_quantize_desc_validate(const migemm_quantize_desc* desc);
+int gemm_quantize_plan_create(const migemm_quantize_desc* desc, migemm_quantize_plan** out);
+int gemm_quantize_plan_destroy(migemm_quantize_plan* plan);
+/* 0: no run needs a workspace. */
+size_t gemm_quantize_workspace_size(const migemm_quantize_plan* plan);
+
+/* The kernel a plan has chosen (for tuning and tests): the waves that share a
+ * row and the 16-byte vectors of it that each lane holds. */
+typedef struct migemm_quantize_info {
+  int32_t waves, vectors;
+  int32_t cu_count;
+} migemm_quantize_info;
+int gemm_quantize_plan_get_info(const migemm_quantize_plan* plan, migemm_quantize_info* info);
+
+/* scale is fp32 [rows]. */
+int gemm_quantize_run(const migemm_quantize_plan* plan, const void* x, void* q, float* scale, void* stream);
+
+/* Block norm: what stands between two blocks of a model, in one pass.  x is a
+ * block's output, z its gate's input, r the residual:
+ *   post_rstd = 1 / sqrt(mean of x^2 + eps),  u = x * post_rstd * post_weight
+ *     (post_norm 0: u = x)
+ *   h = residual_scale * r + branch_scale * sigmoid(z) * u    (z_rs 0: no gate,
+ *     the sigmoid's place is 1)
+ *   rstd = 1 / sqrt(mean of h^2 + eps),  y = h * rstd * weight
+ * y is bf16, or e4m3 or int8 codes with a scale per row, max |y| / 448 or / 127
+ * (the rows that gemm_scaled_run and gemm_int8_run take).  h is rounded to bf16
+ * where it is stored; rstd, y and scale come from it before that.  A row of
+ * zeros gets scale 0 and codes 0.  A row of h with an infinity or a NaN has a
+ * NaN or infinite scale with e4m3, and with int8 a NaN scale and codes 0: its
+ * products hold no number.
+ * Gradients, with h as it was stored, n = h * rstd, s = sigmoid(z), p = x *
+ * post_rstd, g = dy:
+ *   d = dh + rstd * (g * weight - n * mean(g * weight * n))
+ *   dr = bf16(residual_scale * d);  dweight = sum over the rows of g * n (fp32)
+ *   v = branch_scale * d;  dz = bf16(v * u * s * (1 - s))
+ *   dx = bf16(post_rstd * (v * s * post_weight - p * mean(v * s * post_weight * p)))
+ *     (post_norm 0: bf16(v * s));  dpost_weight = sum over the rows of v * s * p
+ * Sums are fp32: rows whose sum of squares passes 3e38 overflow.  cols is
+ * 1 .. 16384 (above: UNSUPPORTED); rows may be 0. */
+typedef struct migemm_block_norm_desc {
+  int64_t rows, cols;
+  int64_t x_rs, r_rs, h_rs;    /* bf16 */
+  int64_t y_rs;                /* y_type */
+  int64_t z_rs;                /* the gate's input (bf16); 0: no gate */
+  int64_t dy_rs, dx_rs, dr_rs; /* backward pass (bf16); all 0: none */
+  int64_t dz_rs;               /* with a gate and a backward pass; else 0 */
+  int64_t dh_rs;               /* the residual's gradient (bf16); 0: none added */
+  float eps;                   /* > 0 and finite */
+  float branch_scale, residual_scale; /* finite */
+  int32_t post_norm;           /* 1: x is normed first; 0: it is not */
+  int32_t y_type;              /* MIGEMM_BF16, MIGEMM_FP8_E4M3 or MIGEMM_INT8 */
+  int32_t device;              /* HIP device ordinal; must be gfx950 */
+} migemm_block_norm_desc;
+
+typedef struct migemm_block_norm_plan migemm_block_norm_plan; /* opaque, host memory only */
+
+int gemm_block_norm_desc_validate(const migemm_block_norm_desc* desc);
+int gemm_block_norm_plan_create(const migemm_block_norm_desc* desc, migemm_block_norm_plan** out);
+int gemm_block_norm_plan_destroy(migemm_block_norm_plan* plan);
+/* Bytes of workspace the backward pass needs (256-byte aligned): for each of the
+ * workgroups that walk the rows, a row of fp32 column sums, with post_norm two.
+ * 0 for a plan without a backward pass. */
+size_t gemm_block_norm_workspace_size(const migemm_block_norm_plan* plan);
+
+/* The kernels a plan has chosen, as migemm_norm_info. */
+typedef struct migemm_block_norm_info {
+  int32_t forward_waves, forward_vectors;
+  int32_t backward_waves, backward_vectors;
+  int32_t backward_workgroups;
+  int32_t cu_count;
+} migemm_block_norm_info;
+int gemm_block_norm_plan_get_info(const migemm_block_norm_plan* plan, migemm_block_norm_info* info);
+
+/* z is given exactly when the plan has a gate, post_weight and post_rstd exactly
+ * with post_norm, scale (fp32 [rows]) exactly when y is 8-bit.  post_weight and
+ * weight are bf16 [cols], 16-byte aligned; post_rstd and rstd fp32 [rows].  h
+ * may be x, z or r itself (same strides), and a bf16 y another of them. */
+int gemm_block_norm_run(const migemm_block_norm_plan* plan, const void* x, const void* z, const void* r,
+                        const void* post_weight, const void* weight, void* h, void* y, float* scale,
+                        float* post_rstd, float* rstd, void* stream);
+
+/* h, post_rstd and rstd are what the forward pass wrote.  dh is given exactly
+ * when the plan has dh_rs; x may be NULL in a plan with neither a gate nor
+ * post_norm.  dx, dr and dz may each be one of the bf16 matrices that come in
+ * (same strides).  dweight and dpost_weight are fp32 [cols], written whole
+ * (zeros for no rows); dpost_weight is given exactly with post_norm. */
+int gemm_block_norm_run_backward(const migemm_block_norm_plan* plan, const void* dy, const void* dh,
+                                 const void* x, const void* z, const void* h, const void* post_weight,
+                                 const void* weight, const float* post_rstd, const float* rstd, void* dx,
+                                 void* dz, void* dr, float* dpost_weight, float* dweight, void* workspace,
+                                 void* stream);
+
+/* Checkpoint: activations x (tokens x cols, bf16) kept in 8 bits for the
+ * backward pass, and the gradient of the weights (out_cols x cols) of the
+ * product that took them, from the kept form.
+ * The kept form is e4m3 codes with a power of two for each 32 tokens of a
+ * column (the last group may have fewer), the least that brings the group's
+ * largest magnitude to 448 or below, but from 2^-109 to 2^119:
+ *   e = that power's exponent + 127 (18 .. 246),  code = e4m3(x * 2^(127 - e))
+ * rounded to nearest, ties to even; past 448 (x past 1.75 * 2^127) the code is
+ * 448's.  An infinity or a NaN becomes the code NaN and does not count for the
+ * power.  In memory: the codes [tokens / 16][ld][16 tokens], tokens rounded up
+ * to 32 and ld = cols rounded up to 16, then the bytes e [tokens / 32][ld];
+ * codes of tokens and columns past the last are 0 (e of such columns 18).
+ *   weight_gradient: dw = sum over the tokens of dy[t][n] * code * 2^(e - 127)
+ * dy is tokens x out_cols bf16; the products are exact and the sums fp32; dw is
+ * out_cols x cols, bf16 (rounded once), or fp32, to which with accumulate the
+ * sum is added.  tokens may be 0 (the gradient is then 0, or unchanged).
+ * tokens below 2^31 - 64; 256 rows of dy and dw span less than 2^31 bytes. */
+typedef struct migemm_checkpoint_desc {
+  int64_t tokens, cols;
+  int64_t x_rs;               /* bf16 */
+  int64_t out_cols;           /* the weights' gradient; these three 0: none */
+  int64_t dy_rs, dw_rs;       /* dy: bf16; dw: dw_type */
+  int32_t dw_type;            /* MIGEMM_BF16 or MIGEMM_FP32 */
+  int32_t accumulate;         /* 1: dw is added to (fp32 only); 0: written */
+  int32_t device;
+  int32_t reserved;           /* must be 0 */
+} migemm_checkpoint_desc;
+
+typedef struct migemm_checkpoint_plan migemm_checkpoint_plan; /* opaque, host memory only */
+
+int gemm_checkpoint_desc_validate(const migemm_checkpoint_desc* desc);
+int gemm_checkpoint_plan_create(const migemm_checkpoint_desc* desc, migemm_checkpoint_plan** out);
+int gemm_checkpoint_plan_destroy(migemm_checkpoint_plan* plan);
+/* Bytes of the kept form (16-byte aligned): one a token and column, and 1 / 32. */
+size_t gemm_checkpoint_size(const migemm_checkpoint_plan* plan);
+/* Bytes of workspace that weight_gradient needs (256-byte aligned); 0: it may
+ * be NULL. */
+size_t gemm_checkpoint_workspace_size(const migemm_checkpoint_plan* plan);
+
+/* Where the kept form's parts lie, and the gradient's kernel (for tuning and
+ * tests; its fields are 0 without one). */
+typedef struct migemm_checkpoint_info {
+  int64_t code_bytes, scale_bytes;
+  int32_t tile_m, tile_n; /* rows and columns of dw a workgroup takes at a time */
+  int32_t lds_stages;     /* stages of 64 tokens in LDS at once */
+  int32_t splits;         /* ranges of the tokens, added up by a second launch if more than 1 */
+  int32_t cu_count;
+  int32_t reserved;
+} migemm_checkpoint_info;
+int gemm_checkpoint_plan_get_info(const migemm_checkpoint_plan* plan, migemm_checkpoint_info* info);
+
+int gemm_checkpoint_pack(const migemm_checkpoint_plan* plan, const void* x, void* kept, void* stream);
+/* x = bf16(code * 2^(e - 127)), exactly. */
+int gemm_checkpoint_unpack(const migemm_checkpoint_plan* plan, const void* kept, void* x, void* stream);
+int gemm_checkpoint_weight_gradient(const migemm_checkpoint_plan* plan, const void* dy, const void* kept,
+                                    void* dw, void* workspace, void* stream);
 
 /* Static text for a status code (never NULL).  No counterpart on the pages. */
 const char* gemm_status_string(int status);

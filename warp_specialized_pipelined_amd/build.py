@@ -21,8 +21,9 @@ ARCH = "gfx950"
 SOURCES = [os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "gemm_kernels.hip")]
 # The operators around the product: their C ABI layer and kernel units.
 OPERATORS = os.path.join(CSRC, "operators")
-OPERATOR_API = os.path.join(OPERATORS, "operators_api.cpp")
-OPERATOR_KERNELS = ["norm_kernels", "scaled_kernels", "loss_kernels"]
+OPERATOR_APIS = ["operators_api", "block_api"]
+OPERATOR_KERNELS = ["norm_kernels", "scaled_kernels", "loss_kernels", "int8_kernels", "quantize_kernels",
+                    "block_norm_kernels", "checkpoint_kernels"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -71,14 +72,15 @@ def build(verbose: bool = False, asan: bool = True) -> str:
     from concurrent.futures import ThreadPoolExecutor
     kernels = {_obj("gemm_kernels.o"): os.path.join(CSRC, "gemm_kernels.hip")}
     kernels.update({_obj(n + ".o"): os.path.join(OPERATORS, n + ".hip") for n in OPERATOR_KERNELS})
-    api = {_obj("api.o"): SOURCES[0], _obj("operators_api.o"): OPERATOR_API}
+    api = {_obj("api.o"): SOURCES[0]}
+    api.update({_obj(n + ".o"): os.path.join(OPERATORS, n + ".cpp") for n in OPERATOR_APIS})
     jobs = [[hipcc(), *HIPCC_FLAGS, "-c", "-o", o, src] for o, src in {**kernels, **api}.items()]
     sapi = []
     if asan:
         for o, src in list(api.items()):
             sapi.append(o[:-2] + "_asan.o")
             jobs.append([hipcc(), *HIPCC_FLAGS, *ASAN_HOST_FLAGS, "-c", "-o", sapi[-1], src])
-    with ThreadPoolExecutor(4) as pool:
+    with ThreadPoolExecutor(8) as pool:
         list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
     tmp = LIB + ".tmp%d" % os.getpid()
     _run([hipcc(), *HIPCC_FLAGS, "-shared", "-o", tmp, *api, *kernels], verbose)

@@ -14,6 +14,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -137,6 +138,17 @@ __device__ __forceinline__ f32x16 mfma_bf16_32x32x16(bf16x8 a, bf16x8 b, f32x16 
 // holds 32 bytes (k values) of row l%32 of A and column l%32 of B.
 __device__ __forceinline__ f32x16 mfma_fp8_32x32x64(i32x8 a, i32x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// D(32x32 int32) += A(32x64 int8) * B(64x32 int8) in two instructions of 32 k.
+// Lane l holds 32 bytes (k values) of row l%32 of A and column l%32 of B: 16
+// for each instruction.  The int32 sums travel as the bits of an fp32 vector,
+// the accumulators' type.
+__device__ __forceinline__ f32x16 mfma_i8_32x32x64(i32x8 a, i32x8 b, f32x16 c) {
+  i32x16 s = __builtin_bit_cast(i32x16, c);
+  s = __builtin_amdgcn_mfma_i32_32x32x32_i8(i32x4{a[0], a[1], a[2], a[3]}, i32x4{b[0], b[1], b[2], b[3]}, s, 0, 0, 0);
+  s = __builtin_amdgcn_mfma_i32_32x32x32_i8(i32x4{a[4], a[5], a[6], a[7]}, i32x4{b[4], b[5], b[6], b[7]}, s, 0, 0, 0);
+  return __builtin_bit_cast(f32x16, s);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

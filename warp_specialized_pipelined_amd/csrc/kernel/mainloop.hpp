@@ -454,7 +454,8 @@ struct FragReader<1, false> {
 // The fragments of two k-steps (buffer kb holds k-steps of parity kb): BM A
 // and 4 B fragments each (64 VGPRs for bf16 with BM = 4, 128 for e4m3).
 // BM is the wave's count of 32-row blocks: 4 (256-row tiles) or 3 (192).
-template <int ES, bool AK, bool BK, int BM = 4>
+// INT8: the bytes are int8, the sums int32 (mfma_i8_32x32x64).
+template <int ES, bool AK, bool BK, int BM = 4, bool INT8 = false>
 struct Frags {
   typedef FragReader<ES, AK, BM> RA;
   typedef FragReader<ES, BK> RB;
@@ -488,7 +489,8 @@ struct Frags {
     static_for<FIRST, FIRST + COUNT>([&](auto mc) {
       constexpr int m = decltype(mc)::value;
       constexpr int i = m >> 2, j = m & 3;
-      acc.v[i][j] = mfma<ES>(b[KB][j], a[KB][i], acc.v[i][j]);
+      if constexpr (INT8) acc.v[i][j] = mfma_i8_32x32x64(b[KB][j], a[KB][i], acc.v[i][j]);
+      else acc.v[i][j] = mfma<ES>(b[KB][j], a[KB][i], acc.v[i][j]);
     });
   }
 };
@@ -526,12 +528,13 @@ struct Frags {
 // segment); K is the problem's K or, for a segment that ends before it, the
 // segment's end: loads past it fall out of range like loads past the
 // problem's K.  Only the first BM rows of blocks of acc are used.
-template <int ES, bool AK, bool BK, int BM = 4, class SideWork>
+template <int ES, bool AK, bool BK, int BM = 4, bool INT8 = false, class SideWork>
 __device__ __forceinline__ void mainloop_range(Accum& acc, const KernelArgs& a, int tm, int tn,
                                                int wave, int lane, SideWork& side, int k0, int KT,
                                                int64_t K) {
   typedef StageGeom<ES> G;
-  typedef Frags<ES, AK, BK, BM> FW;
+  typedef Frags<ES, AK, BK, BM, INT8> FW;
+  static_assert(!INT8 || ES == 1, "int8 operands are bytes");
   static_assert(BM == 4 || (BM == 3 && (ES == 2 || (AK && BK))), "192-row tiles: bf16, or K-contiguous operands");
   static_assert(BM == 4 || !SideWork::kLoadsC, "C is read in the K loop of 256-row tiles only");
   constexpr bool kBf16 = ES == 2;
@@ -706,7 +709,7 @@ __device__ __forceinline__ void mainloop_range(Accum& acc, const KernelArgs& a, 
 }
 
 // The whole K loop of one output tile (BM: the wave's 32-row blocks).
-template <int ES, bool AK, bool BK, int BM = 4, class SideWork>
+template <int ES, bool AK, bool BK, int BM = 4, bool INT8 = false, class SideWork>
 __device__ __forceinline__ void mainloop(Accum& acc, const KernelArgs& a, int tm, int tn,
                                          int wave, int lane, SideWork& side) {
   int KT = (int)((a.K + StageGeom<ES>::kK - 1) / StageGeom<ES>::kK);
@@ -714,7 +717,7 @@ __device__ __forceinline__ void mainloop(Accum& acc, const KernelArgs& a, int tm
   // are used, not once before the tile loop and held (or spilled, and
   // reloaded with a vmcnt(0)) across it.
   asm volatile("" : "+s"(KT));
-  mainloop_range<ES, AK, BK, BM>(acc, a, tm, tn, wave, lane, side, 0, KT, a.K);
+  mainloop_range<ES, AK, BK, BM, INT8>(acc, a, tm, tn, wave, lane, side, 0, KT, a.K);
 }
 
 }  // namespace migemm

@@ -194,10 +194,13 @@ struct MidAccum {
   f32x16 v[BM][BN];
 };
 
+// How bytes are multiplied: as e4m3 by its own instructions, through bf16
+// (rowblock.hpp), or as int8 (sums: int32 bits).
+enum MidMul { kMulNative, kMulExact, kMulInt8 };
+
 // K stages [k0, k0 + KT) of the tile at (m0, n0); loads past kend (at most K)
-// read as zero.  EXACT: e4m3 through bf16.  On return every wave is done with
-// the ring.
-template <int ES, bool AK, bool BK, int TM, int TN, int SLOTS, bool EXACT = false>
+// read as zero.  On return every wave is done with the ring.
+template <int ES, bool AK, bool BK, int TM, int TN, int SLOTS, MidMul MUL = kMulNative>
 __device__ __forceinline__ void mid_loop(MidAccum<TM / 64, TN / 64>& acc, const KernelArgs& a, int64_t m0,
                                          int64_t n0, int wave, int lane, int k0, int KT, int64_t kend) {
   typedef StageGeom<ES> G;
@@ -233,11 +236,12 @@ __device__ __forceinline__ void mid_loop(MidAccum<TM / 64, TN / 64>& acc, const 
     else fb[b][f][x - BM] = rb.template read<x - BM, ks>(slot + T::kPartA);
   };
   // Product m of the k-step in buffer b, place f.
-  WideFrag wa[EXACT ? BM : 1], wb[EXACT ? BN : 1];
+  constexpr bool kExact = MUL == kMulExact;
+  WideFrag wa[kExact ? BM : 1], wb[kExact ? BN : 1];
   auto multiply = [&](auto bc, auto fc, auto mc) {
     constexpr int b = decltype(bc)::value, f = decltype(fc)::value;
     constexpr int i = decltype(mc)::value / BN, j = decltype(mc)::value % BN;
-    if constexpr (EXACT) {
+    if constexpr (kExact) {
       if constexpr (i == 0 && j == 0) {
 #pragma unroll
         for (int x = 0; x < BM; ++x) wa[x] = widen_frag(fa[b][f][x]);
@@ -246,6 +250,8 @@ __device__ __forceinline__ void mid_loop(MidAccum<TM / 64, TN / 64>& acc, const 
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc.v[i][j] = mfma<2>(wb[j].v[q], wa[i].v[q], acc.v[i][j]);
+    } else if constexpr (MUL == kMulInt8) {
+      acc.v[i][j] = mfma_i8_32x32x64(fb[b][f][j], fa[b][f][i], acc.v[i][j]);
     } else {
       acc.v[i][j] = mfma<ES>(fb[b][f][j], fa[b][f][i], acc.v[i][j]);
     }
@@ -413,8 +419,8 @@ __device__ __forceinline__ void mid_add_all(const mid_piece* sums, int64_t item,
       for (int c = 0; c < 4; ++c) acc.v[b / BN][b % BN][4 * q + c] += x[c];
     }
 }
-// Adds one block of such sums to acc.
-template <int BM, int BN>
+// Adds one block of such sums to acc (INT: int32 bits, acc's too).
+template <int BM, int BN, bool INT = false>
 __device__ __forceinline__ void mid_add(const mid_piece* sums, int64_t item, MidAccum<1, 1>& acc, int wave,
                                         int block, int lane) {
   const mid_piece* p = sums + ((item * 4 + wave) * BM * BN + block) * 256 + lane;
@@ -422,7 +428,10 @@ __device__ __forceinline__ void mid_add(const mid_piece* sums, int64_t item, Mid
   for (int q = 0; q < 4; ++q) {
     const mid_piece x = p[64 * q];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc.v[0][0][4 * q + c] += x[c];
+    for (int c = 0; c < 4; ++c) {
+      const float v = acc.v[0][0][4 * q + c];
+      acc.v[0][0][4 * q + c] = INT ? __int_as_float(__float_as_int(v) + __float_as_int(x[c])) : v + x[c];
+    }
   }
 }
 // Four results of a row, rounded to bf16, where `left` columns are left from

@@ -45,6 +45,51 @@ int64_t norm_partial_rows(int64_t rows, int64_t cols, int cu_count);
 hipError_t launch_norm_forward(const NormArgs& a, bool e4m3, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream);
 
+// --------------------------------------------------------------- quantize
+
+struct QuantizeArgs {
+  const void* x;  // bf16
+  void* q;        // e4m3 or int8
+  float* scale;
+  int64_t rows, cols;
+  int64_t x_rs, q_rs;  // elements
+};
+hipError_t launch_quantize(const QuantizeArgs& a, bool e4m3, hipStream_t stream);
+
+// ------------------------------------------------------------- block norm
+
+struct BlockNormArgs {
+  const void* x;            // bf16, like every matrix but y
+  const void* z;            // the gate (NULL: none)
+  const void* r;            // forward
+  const void* dy;           // backward
+  const void* dh;           // backward (NULL: none)
+  const void* post_weight;  // bf16 [cols] (NULL: no norm behind the block)
+  const void* weight;
+  void* h;                  // forward: out; backward: in
+  void* y;                  // forward: bf16, e4m3 or int8
+  void* dx;                 // backward
+  void* dz;
+  void* dr;
+  float* scale;             // forward, e4m3 and int8
+  float* post_rstd;         // forward: out; backward: in
+  float* rstd;
+  float* dpost_weight;      // backward
+  float* dweight;
+  float* partials;          // backward: workspace, one row of sums per row walker
+  int64_t rows, cols;
+  int64_t x_rs, z_rs, r_rs, h_rs, y_rs, dy_rs, dh_rs, dx_rs, dz_rs, dr_rs;  // elements
+  int64_t partial_rows;
+  float eps, branch, residual;
+};
+
+// Widest row the kernels hold in registers.
+constexpr int64_t kBlockNormMaxCols = 16 * 64 * 2 * 8;
+
+// y_type: 0 bf16, 1 e4m3, 2 int8.
+hipError_t launch_block_norm_forward(const BlockNormArgs& a, int y_type, hipStream_t stream);
+hipError_t launch_block_norm_backward(const BlockNormArgs& a, hipStream_t stream);
+
 // ----------------------------------------------------------------- scaled
 
 // Four fp32 sums.
@@ -54,6 +99,7 @@ struct ScaledArgs {
   KernelArgs gemm;       // A, B: e4m3, K-contiguous; strides in elements
   const float* a_scale;  // [M]
   const float* b_scale;  // [N], 16-byte aligned
+  const float* bias;     // int8: [N], 16-byte aligned (NULL: none)
   mid_piece* partials;   // workspace: the splits' sums
   int32_t splits;
 };
@@ -74,6 +120,35 @@ struct ScaledKernel {
 ScaledKernel scaled_kernel(int variant);
 hipError_t prepare_scaled();
 hipError_t launch_scaled(const ScaledArgs& a, int variant, int cu_count, hipStream_t stream);
+
+// The same of int8 (A, B: int8).
+ScaledChoice choose_int8(int64_t M, int64_t N, int64_t K, int cu_count);
+ScaledKernel int8_kernel(int variant);
+hipError_t prepare_int8();
+hipError_t launch_int8(const ScaledArgs& a, int variant, int cu_count, hipStream_t stream);
+
+// ------------------------------------------------------------- checkpoint
+
+// The kept activations of T tokens x `cols`: e4m3 codes [tokens / 16][ld][16
+// tokens] for T rounded up to 32 tokens and ld = cols rounded up to 16, then
+// a byte for each 32 tokens and column, [tokens / 32][ld]: the exponent of a
+// power of two, plus 127.
+struct CheckpointArgs {
+  const void* x;          // pack: in (bf16)
+  void* x_out;            // unpack: out
+  unsigned char* codes;
+  unsigned char* scales;
+  int64_t tokens, cols, ld;
+  int64_t x_rs;           // elements
+  // The weights' gradient dw (out_cols x cols) = dy^T (kept activations).
+  const void* dy;         // tokens x out_cols, bf16
+  void* dw;               // bf16 or fp32
+  int64_t out_cols, dy_rs, dw_rs;
+  bool fp32, accumulate;  // accumulate: dw += (fp32)
+};
+hipError_t launch_checkpoint_pack(const CheckpointArgs& a, hipStream_t stream);
+hipError_t launch_checkpoint_unpack(const CheckpointArgs& a, hipStream_t stream);
+hipError_t launch_checkpoint_gradient(const CheckpointArgs& a, hipStream_t stream);
 
 // ------------------------------------------------------------------- loss
 

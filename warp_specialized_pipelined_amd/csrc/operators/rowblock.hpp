@@ -56,6 +56,12 @@ __device__ __forceinline__ void widen(i32x4 x, i32x4& lo, i32x4& hi) {
   }
 }
 constexpr int kExactE4M3 = 3;  // in place of an element size: e4m3 through bf16
+constexpr int kInt8 = 4;       // and int8, whose int32 sums travel as fp32 bits
+__device__ __forceinline__ f32x4 mfma_16(i32x4 b0, i32x4 b1, i32x4 a0, i32x4 a1, f32x4 c,
+                                         std::integral_constant<int, kInt8>) {
+  const i32x4 s = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0, a0, __builtin_bit_cast(i32x4, c), 0, 0, 0);
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(b1, a1, s, 0, 0, 0));
+}
 __device__ __forceinline__ f32x4 mfma_16(i32x4 b0, i32x4 b1, i32x4 a0, i32x4 a1, f32x4 c,
                                          std::integral_constant<int, kExactE4M3>) {
   const std::integral_constant<int, 2> bf16;
@@ -162,17 +168,18 @@ __device__ __forceinline__ void rowblock_loop(f32x4 (&acc)[MB][NB], const RowBlo
 
 // The waves' partial tiles are added in the order of the waves: block
 // mb * NB + nb is summed by wave (mb * NB + nb) % W, which then calls
-// done(mb, nb, sum).  `part` holds W MB NB * 64 pieces of 16 bytes.
-template <int MB, int NB, int W, class Done>
-__device__ __forceinline__ void rowblock_join(const f32x4 (&acc)[MB][NB], f32x4* part, int wave,
+// done(mb, nb, sum).  `part` holds W MB NB * 64 pieces of 16 bytes, of type V
+// (i32x4 for int8: the bits that acc holds).
+template <int MB, int NB, int W, class V, class Done>
+__device__ __forceinline__ void rowblock_join(const f32x4 (&acc)[MB][NB], V* part, int wave,
                                               int lane, Done&& done) {
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int n = 0; n < NB; ++n) part[(wave * MB * NB + m * NB + n) * 64 + lane] = acc[m][n];
+    for (int n = 0; n < NB; ++n) part[(wave * MB * NB + m * NB + n) * 64 + lane] = __builtin_bit_cast(V, acc[m][n]);
   __syncthreads();
   for (int b = wave; b < MB * NB; b += W) {
-    f32x4 sum = part[b * 64 + lane];
+    V sum = part[b * 64 + lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) sum += part[(w * MB * NB + b) * 64 + lane];
     done(b / NB, b % NB, sum);

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(_HERE, "libmigemm.so")
 
 MIGEMM_BF16 = 1
 MIGEMM_FP8_E4M3 = 2
+MIGEMM_INT8 = 3
+MIGEMM_FP32 = 4
 
 MIGEMM_OK = 0
 MIGEMM_ERR_INVALID_ARG = -1
@@ -48,6 +50,16 @@ EXPORTED = [
     "gemm_scaled_workspace_size", "gemm_scaled_plan_get_info", "gemm_scaled_run",
     "gemm_vocab_loss_desc_validate", "gemm_vocab_loss_plan_create", "gemm_vocab_loss_plan_destroy",
     "gemm_vocab_loss_workspace_size", "gemm_vocab_loss_plan_get_info", "gemm_vocab_loss_run", "gemm_vocab_loss_run_backward",
+    "gemm_int8_desc_validate", "gemm_int8_plan_create", "gemm_int8_plan_destroy",
+    "gemm_int8_workspace_size", "gemm_int8_plan_get_info", "gemm_int8_run",
+    "gemm_quantize_desc_validate", "gemm_quantize_plan_create", "gemm_quantize_plan_destroy",
+    "gemm_quantize_workspace_size", "gemm_quantize_plan_get_info", "gemm_quantize_run",
+    "gemm_block_norm_desc_validate", "gemm_block_norm_plan_create", "gemm_block_norm_plan_destroy",
+    "gemm_block_norm_workspace_size", "gemm_block_norm_plan_get_info", "gemm_block_norm_run",
+    "gemm_block_norm_run_backward",
+    "gemm_checkpoint_desc_validate", "gemm_checkpoint_plan_create", "gemm_checkpoint_plan_destroy",
+    "gemm_checkpoint_size", "gemm_checkpoint_workspace_size", "gemm_checkpoint_plan_get_info",
+    "gemm_checkpoint_pack", "gemm_checkpoint_unpack", "gemm_checkpoint_weight_gradient",
 ]
 
 
@@ -137,6 +149,54 @@ class migemm_vocab_loss_info(ctypes.Structure):
         "cu_count", "pieces")] + [("piece", ctypes.c_int64)]
 
 
+class migemm_int8_desc(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("a_rs", ctypes.c_int64), ("b_cs", ctypes.c_int64), ("d_rs", ctypes.c_int64),
+        ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class migemm_int8_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tile_m", "tile_n", "lds_stages", "splits", "cu_count")]
+
+
+class migemm_quantize_desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("x_rs", ctypes.c_int64), ("q_rs", ctypes.c_int64),
+        ("q_type", ctypes.c_int32), ("device", ctypes.c_int32), ("reserved", ctypes.c_int64),
+    ]
+
+
+class migemm_quantize_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("waves", "vectors", "cu_count")]
+
+
+class migemm_block_norm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "rows", "cols", "x_rs", "r_rs", "h_rs", "y_rs", "z_rs", "dy_rs", "dx_rs", "dr_rs", "dz_rs", "dh_rs")] + [
+        ("eps", ctypes.c_float), ("branch_scale", ctypes.c_float), ("residual_scale", ctypes.c_float),
+        ("post_norm", ctypes.c_int32), ("y_type", ctypes.c_int32), ("device", ctypes.c_int32),
+    ]
+
+
+class migemm_block_norm_info(ctypes.Structure):
+    _fields_ = migemm_norm_info._fields_
+
+
+class migemm_checkpoint_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "cols", "x_rs", "out_cols", "dy_rs", "dw_rs")] + [
+        ("dw_type", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+        ("device", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class migemm_checkpoint_info(ctypes.Structure):
+    _fields_ = [("code_bytes", ctypes.c_int64), ("scale_bytes", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("tile_m", "tile_n", "lds_stages", "splits", "cu_count", "reserved")]
+
+
 class MigemmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -202,6 +262,16 @@ def load(path: str | None = None):
     lib.gemm_vocab_loss_run.restype = i32
     lib.gemm_vocab_loss_run_backward.argtypes = [vp] * 10
     lib.gemm_vocab_loss_run_backward.restype = i32
+    _declare_plan_calls(lib, "int8", migemm_int8_desc, migemm_int8_info)
+    _declare_plan_calls(lib, "quantize", migemm_quantize_desc, migemm_quantize_info)
+    _declare_plan_calls(lib, "block_norm", migemm_block_norm_desc, migemm_block_norm_info)
+    _declare_plan_calls(lib, "checkpoint", migemm_checkpoint_desc, migemm_checkpoint_info)
+    lib.gemm_checkpoint_size.argtypes = [vp]
+    lib.gemm_checkpoint_size.restype = ctypes.c_size_t
+    for name, args in (("int8_run", 9), ("quantize_run", 5), ("block_norm_run", 12), ("block_norm_run_backward", 17),
+                       ("checkpoint_pack", 4), ("checkpoint_unpack", 4), ("checkpoint_weight_gradient", 6)):
+        f = getattr(lib, "gemm_" + name)
+        f.argtypes, f.restype = [vp] * args, i32
     lib.gemm_status_string.argtypes = [i32]
     lib.gemm_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -437,6 +507,84 @@ def gemm_vocab_loss_run_backward(plan, x, w, target, lse, dloss, dx, dw, workspa
     return int(st)
 
 
+def gemm_int8_desc_validate(desc: migemm_int8_desc) -> int:
+    return int(load().gemm_int8_desc_validate(ctypes.byref(desc)))
+
+
+def gemm_int8_run(plan, a, a_scale, b, b_scale, bias, d, workspace=None, stream=None, check: bool = True) -> int:
+    st = (_lib or load()).gemm_int8_run(_plan(plan), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(bias),
+                                        _ptr(d), _ptr(workspace), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_int8_run")
+    return int(st)
+
+
+def gemm_quantize_desc_validate(desc: migemm_quantize_desc) -> int:
+    return int(load().gemm_quantize_desc_validate(ctypes.byref(desc)))
+
+
+def gemm_quantize_run(plan, x, q, scale, stream=None, check: bool = True) -> int:
+    st = (_lib or load()).gemm_quantize_run(_plan(plan), _ptr(x), _ptr(q), _ptr(scale), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_quantize_run")
+    return int(st)
+
+
+def gemm_block_norm_desc_validate(desc: migemm_block_norm_desc) -> int:
+    return int(load().gemm_block_norm_desc_validate(ctypes.byref(desc)))
+
+
+def gemm_block_norm_run(plan, x, z, r, post_weight, weight, h, y, scale, post_rstd, rstd, stream=None,
+                        check: bool = True) -> int:
+    st = (_lib or load()).gemm_block_norm_run(
+        _plan(plan), _ptr(x), _ptr(z), _ptr(r), _ptr(post_weight), _ptr(weight), _ptr(h), _ptr(y), _ptr(scale),
+        _ptr(post_rstd), _ptr(rstd), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_block_norm_run")
+    return int(st)
+
+
+def gemm_block_norm_run_backward(plan, dy, dh, x, z, h, post_weight, weight, post_rstd, rstd, dx, dz, dr,
+                                 dpost_weight, dweight, workspace=None, stream=None, check: bool = True) -> int:
+    st = (_lib or load()).gemm_block_norm_run_backward(
+        _plan(plan), _ptr(dy), _ptr(dh), _ptr(x), _ptr(z), _ptr(h), _ptr(post_weight), _ptr(weight),
+        _ptr(post_rstd), _ptr(rstd), _ptr(dx), _ptr(dz), _ptr(dr), _ptr(dpost_weight), _ptr(dweight),
+        _ptr(workspace), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_block_norm_run_backward")
+    return int(st)
+
+
+def gemm_checkpoint_desc_validate(desc: migemm_checkpoint_desc) -> int:
+    return int(load().gemm_checkpoint_desc_validate(ctypes.byref(desc)))
+
+
+def gemm_checkpoint_size(plan) -> int:
+    return int(load().gemm_checkpoint_size(_plan(plan)))
+
+
+def gemm_checkpoint_pack(plan, x, kept, stream=None, check: bool = True) -> int:
+    st = (_lib or load()).gemm_checkpoint_pack(_plan(plan), _ptr(x), _ptr(kept), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_checkpoint_pack")
+    return int(st)
+
+
+def gemm_checkpoint_unpack(plan, kept, x, stream=None, check: bool = True) -> int:
+    st = (_lib or load()).gemm_checkpoint_unpack(_plan(plan), _ptr(kept), _ptr(x), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_checkpoint_unpack")
+    return int(st)
+
+
+def gemm_checkpoint_weight_gradient(plan, dy, kept, dw, workspace=None, stream=None, check: bool = True) -> int:
+    st = (_lib or load()).gemm_checkpoint_weight_gradient(_plan(plan), _ptr(dy), _ptr(kept), _ptr(dw),
+                                                          _ptr(workspace), _stream(stream))
+    if check and st != MIGEMM_OK:
+        raise MigemmError(st, "gemm_checkpoint_weight_gradient")
+    return int(st)
+
+
 class _OperatorPlan:
     """Owns an operator's plan handle; destroys it when garbage-collected."""
 
@@ -524,3 +672,86 @@ class VocabLossPlan(_OperatorPlan):
 
     def run_backward(self, x, w, target, lse, dloss, dx, dw, workspace=None, stream=None):
         return gemm_vocab_loss_run_backward(self, x, w, target, lse, dloss, dx, dw, workspace, stream)
+
+
+class Int8Plan(_OperatorPlan):
+    """d (M x N bf16) = a (M x K int8, a scale per row) times the transpose of
+    b (N x K int8, a scale per row), plus a bias per column or None; row
+    strides in elements."""
+
+    kind = "int8"
+    info_type = migemm_int8_info
+
+    def __init__(self, M, N, K, *, a_rs, b_cs, d_rs, device=0):
+        super().__init__(migemm_int8_desc(M, N, K, a_rs, b_cs, d_rs, device, 0))
+
+    def run(self, a, a_scale, b, b_scale, bias, d, workspace=None, stream=None):
+        return gemm_int8_run(self, a, a_scale, b, b_scale, bias, d, workspace, stream)
+
+
+class QuantizePlan(_OperatorPlan):
+    """bf16 rows x cols to int8 or e4m3 with a scale per row; row strides in
+    elements."""
+
+    kind = "quantize"
+    info_type = migemm_quantize_info
+
+    def __init__(self, rows, cols, q_type=MIGEMM_INT8, *, x_rs, q_rs, device=0):
+        super().__init__(migemm_quantize_desc(rows, cols, x_rs, q_rs, q_type, device, 0))
+
+    def run(self, x, q, scale, stream=None):
+        return gemm_quantize_run(self, x, q, scale, stream)
+
+
+class BlockNormPlan(_OperatorPlan):
+    """Between two blocks of rows x cols: the norm of a block's output x
+    (post_norm), its gate sigmoid(z) (z_rs) and scale, the residual's addition
+    and the next block's norm, y in bf16, e4m3 or int8; row strides in
+    elements.  dy_rs, dx_rs and dr_rs (dz_rs with a gate, and dh_rs): with a
+    backward pass."""
+
+    kind = "block_norm"
+    info_type = migemm_block_norm_info
+
+    def __init__(self, rows, cols, eps, y_type=MIGEMM_BF16, *, x_rs, r_rs, h_rs, y_rs, z_rs=0, post_norm=True,
+                 branch_scale=1.0, residual_scale=1.0, dy_rs=0, dh_rs=0, dx_rs=0, dr_rs=0, dz_rs=0, device=0):
+        super().__init__(migemm_block_norm_desc(rows, cols, x_rs, r_rs, h_rs, y_rs, z_rs, dy_rs, dx_rs, dr_rs, dz_rs,
+                                                dh_rs, eps, branch_scale, residual_scale, int(post_norm), y_type,
+                                                device))
+
+    def run(self, x, z, r, post_weight, weight, h, y, scale, post_rstd, rstd, stream=None):
+        return gemm_block_norm_run(self, x, z, r, post_weight, weight, h, y, scale, post_rstd, rstd, stream)
+
+    def run_backward(self, dy, dh, x, z, h, post_weight, weight, post_rstd, rstd, dx, dz, dr, dpost_weight, dweight,
+                     workspace=None, stream=None):
+        return gemm_block_norm_run_backward(self, dy, dh, x, z, h, post_weight, weight, post_rstd, rstd, dx, dz, dr,
+                                            dpost_weight, dweight, workspace, stream)
+
+
+class CheckpointPlan(_OperatorPlan):
+    """tokens x cols activations kept in 8 bits for the backward pass, and the
+    gradient (out_cols x cols) of the weights of the product that took them;
+    row strides in elements.  out_cols, dy_rs and dw_rs: with that gradient;
+    accumulate: added to dw (fp32)."""
+
+    kind = "checkpoint"
+    info_type = migemm_checkpoint_info
+
+    def __init__(self, tokens, cols, *, x_rs, out_cols=0, dy_rs=0, dw_rs=0, dw_type=MIGEMM_BF16, accumulate=False,
+                 device=0):
+        super().__init__(migemm_checkpoint_desc(tokens, cols, x_rs, out_cols, dy_rs, dw_rs, dw_type,
+                                                int(accumulate), device, 0))
+
+    @property
+    def checkpoint_size(self) -> int:
+        """Bytes of the kept form."""
+        return gemm_checkpoint_size(self.handle)
+
+    def pack(self, x, kept, stream=None):
+        return gemm_checkpoint_pack(self, x, kept, stream)
+
+    def unpack(self, kept, x, stream=None):
+        return gemm_checkpoint_unpack(self, kept, x, stream)
+
+    def weight_gradient(self, dy, kept, dw, workspace=None, stream=None):
+        return gemm_checkpoint_weight_gradient(self, dy, kept, dw, workspace, stream)
