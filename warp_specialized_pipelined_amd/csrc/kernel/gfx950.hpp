@@ -72,6 +72,13 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, lds_u8* lds, uin
                "{m0}"(m0)
                : "memory");
 }
+// 4 bytes per lane: lane i writes LDS bytes [lds + 4 i, lds + 4 i + 4).
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, lds_u8* lds, uint32_t voffset) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+  asm volatile("s_nop 1\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voffset), "s"(r),
+               "{m0}"(m0)
+               : "memory");
+}
 // 5 wait states (see above) and the non-temporal hint (nt): for data read
 // once, which should not displace the operand lines that other compute
 // units still need from the L2.

@@ -32,6 +32,7 @@ struct migemm_checkpoint_plan {
   migemm_checkpoint_desc desc;
   int cus;
   int64_t ld, code_bytes, scale_bytes;
+  int variant, splits;
   size_t workspace_bytes;
 };
 
@@ -342,7 +343,7 @@ int gemm_checkpoint_plan_create(const migemm_checkpoint_desc* desc, migemm_check
   if (st != MIGEMM_OK) return st;
   int cus = 0;
   static std::atomic<bool> prepared[kMaxDevices];
-  st = check_device(desc->device, &cus, prepared, nothing);
+  st = check_device(desc->device, &cus, prepared, prepare_checkpoint);
   if (st != MIGEMM_OK) return st;
   migemm_checkpoint_plan* p = new (std::nothrow) migemm_checkpoint_plan();
   if (!p) return MIGEMM_ERR_INVALID_ARG;
@@ -351,6 +352,12 @@ int gemm_checkpoint_plan_create(const migemm_checkpoint_desc* desc, migemm_check
   p->ld = up(desc->cols, 16);
   p->code_bytes = up(desc->tokens, 32) * p->ld;
   p->scale_bytes = p->code_bytes / 32;
+  if (with_gradient(*desc)) {
+    const CheckpointChoice c =
+        choose_checkpoint(desc->tokens, desc->cols, desc->out_cols, desc->dw_type == MIGEMM_FP32 ? 4 : 2, cus);
+    p->variant = c.variant, p->splits = c.splits;
+    p->workspace_bytes = (size_t)c.workspace_bytes;
+  }
   return add_live(p, kCheckpoint, out);
 }
 
@@ -369,6 +376,10 @@ int gemm_checkpoint_plan_get_info(const migemm_checkpoint_plan* p, migemm_checkp
   *out = {};
   out->code_bytes = p->code_bytes, out->scale_bytes = p->scale_bytes;
   out->cu_count = p->cus;
+  if (!with_gradient(p->desc)) return MIGEMM_OK;
+  const CheckpointKernel k = checkpoint_kernel(p->variant);
+  out->tile_m = k.tile_m, out->tile_n = k.tile_n, out->lds_stages = k.lds_stages;
+  out->splits = p->splits;
   return MIGEMM_OK;
 }
 
@@ -406,7 +417,8 @@ int gemm_checkpoint_weight_gradient(const migemm_checkpoint_plan* p, const void*
   CheckpointArgs a = checkpoint_args(p, kept);
   a.dy = dy, a.dw = dw, a.out_cols = d.out_cols, a.dy_rs = d.dy_rs, a.dw_rs = d.dw_rs;
   a.fp32 = d.dw_type == MIGEMM_FP32, a.accumulate = d.accumulate != 0;
-  return launched(launch_checkpoint_gradient(a, static_cast<hipStream_t>(stream)));
+  a.splits = p->splits, a.partials = static_cast<mid_piece*>(workspace);
+  return launched(launch_checkpoint_gradient(a, p->variant, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -13,7 +13,11 @@
 // on the bf16 instructions: the products are exact, the sums fp32.
 #include <hip/hip_runtime.h>
 
+#include <math.h>
+
 #include "../kernel/gfx950.hpp"
+#include "../kernel/scheduler.hpp"
+#include "kepttile.hpp"
 #include "operators.h"
 #include "rows.hpp"
 
@@ -160,50 +164,97 @@ __global__ __launch_bounds__(64) void checkpoint_unpack(CheckpointArgs a, int64_
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) unpack_item(a, i, threadIdx.x);
 }
 
-// A 32 x 32 tile of dw a wave, its operands straight from memory.  Lane l holds
-// column l % 32 of dy (and of the kept activations) and, of a group of 32
-// tokens, 16 (l / 32) .. + 15: eight for each of two instructions.
-__global__ __launch_bounds__(64) void checkpoint_gradient_simple(CheckpointArgs a) {
-  const int lane = threadIdx.x, l = lane & 31, half = lane >> 5;
-  const int64_t across = (a.cols + 31) / 32;
-  const int64_t n0 = blockIdx.x / across * 32, k0 = blockIdx.x % across * 32;
-  const int64_t n = n0 + l, k = k0 + l;
-  const unsigned short* dy = static_cast<const unsigned short*>(a.dy);
-  f32x16 acc = {};
-  for (int64_t t0 = 0; t0 < a.tokens; t0 += 32) {
-    u32x4 code = {0, 0, 0, 0};
-    float scale = 1.0f;
-    if (k < a.ld) {
-      code = *reinterpret_cast<const u32x4*>(a.codes + ((t0 / 16 + half) * a.ld + k) * 16);
-      scale = power_of(a.scales[(t0 / 32) * a.ld + k]);
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 av, bv;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t t = t0 + 16 * half + 8 * s + 2 * q;
-        const uint32_t d0 = n < a.out_cols && t < a.tokens ? dy[t * a.dy_rs + n] : 0;
-        const uint32_t d1 = n < a.out_cols && t + 1 < a.tokens ? dy[(t + 1) * a.dy_rs + n] : 0;
-        av[q] = d0 | d1 << 16;
-        bv[q] = two_bf16(code[2 * s + (q >> 1)], scale, q & 1);
-      }
-      acc = mfma_bf16_32x32x16(__builtin_bit_cast(bf16x8, bv), __builtin_bit_cast(bf16x8, av), acc);
-    }
+// TM x TN tiles of dw (kepttile.hpp), a workgroup for each of a tile's `splits`
+// ranges of the tokens.  With one it stores the result; with more each stores
+// its fp32 sums in register order, and kept_join adds them up.
+template <int TM, int TN, int SLOTS, int WAVES>
+__global__ __launch_bounds__(256, WAVES) void kept_gradient(CheckpointArgs a) {
+  constexpr int BM = TM / 64, BN = TN / 64;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int tiles_m = (int)((a.out_cols + TM - 1) / TM), tiles_n = (int)((a.cols + TN - 1) / TN);
+  const int slot = persistent_slot(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
+  const int split = slot / tiles, tile = slot - split * tiles;
+  const MidTile t = mid_tile(tile, tiles_m, tiles_n);
+  const int stages = (int)((a.tokens + kKeptTokens - 1) / kKeptTokens);
+  const int k0 = (int)((int64_t)stages * split / a.splits), k1 = (int)((int64_t)stages * (split + 1) / a.splits);
+  const int64_t kend = (int64_t)k1 * kKeptTokens < a.tokens ? (int64_t)k1 * kKeptTokens : a.tokens;
+  MidAccum<BM, BN> acc;
+  kept_loop<TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0, k1 - k0, kend);
+  if (a.splits > 1) {
+    mid_put(a.partials, slot, acc, wave, lane);
+    return;
   }
-  if (n >= a.out_cols) return;
+  const int64_t m0 = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM;
+  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN;
+  if (!a.fp32) {
+    mid_store<BM, BN>(
+        a.dw, a.dw_rs, a.out_cols, a.cols, m0, n0, wave, lane,
+        [&](int bi, int bj, int q) {
+          const f32x16& v = acc.v[bi][bj];
+          return f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        },
+        [](int64_t r) { return r; });
+  } else if (a.accumulate) {
+    kept_store32<BM, BN, true>(a, acc, m0, n0, wave, lane);
+  } else {
+    kept_store32<BM, BN, false>(a, acc, m0, n0, wave, lane);
+  }
+}
+
+// The ranges' sums of one 32 x 32 block, added in order and stored: a wave a
+// block.
+template <int TM, int TN>
+__global__ __launch_bounds__(64) void kept_join(CheckpointArgs a) {
+  constexpr int BM = TM / 64, BN = TN / 64;
+  const int lane = threadIdx.x;
+  const int tiles_m = (int)((a.out_cols + TM - 1) / TM), tiles_n = (int)((a.cols + TN - 1) / TN);
+  const int part = blockIdx.x % (4 * BM * BN), tile = blockIdx.x / (4 * BM * BN);
+  const int wave = part / (BM * BN), block = part % (BM * BN);
+  const MidTile t = mid_tile(tile, tiles_m, tiles_n);
+  const int64_t m = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM + 32 * (block / BN) + (lane & 31);
+  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN + 32 * (block % BN);
+  if (m - (lane & 31) >= a.out_cols || n0 >= a.cols) return;
+  MidAccum<1, 1> acc = {};
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i) mid_add<BM, BN>(a.partials, i * tiles_m * tiles_n + tile, acc, wave, block, lane);
+  if (m >= a.out_cols) return;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t col = k0 + 8 * (i >> 2) + 4 * half + (i & 3);
-    if (col >= a.cols) continue;
-    const int64_t at = n * a.dw_rs + col;
-    if (a.fp32) {
-      float* d = static_cast<float*>(a.dw) + at;
-      *d = a.accumulate ? *d + acc[i] : acc[i];
+  for (int q = 0; q < 4; ++q) {
+    const int64_t n = n0 + 8 * q + 4 * (lane >> 5), left = a.cols - n;
+    const f32x16& v = acc.v[0][0];
+    const f32x4 x = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    if (!a.fp32) {
+      store4(static_cast<unsigned short*>(a.dw) + m * a.dw_rs + n, left, x);
     } else {
-      static_cast<unsigned short*>(a.dw)[at] = (unsigned short)pack_bf16x2(acc[i], 0.0f);
+      float* d = static_cast<float*>(a.dw) + m * a.dw_rs + n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) d[e] = a.accumulate ? d[e] + x[e] : x[e];
     }
   }
+}
+
+struct KeptVariant {
+  int tm, tn, slots, lds;
+  void (*kernel)(CheckpointArgs);
+  void (*join)(CheckpointArgs);
+  // What its tiles cost (choose_checkpoint), in microseconds: a stage with one
+  // tile a compute unit and with as many as fit, and a tile besides.
+  int per_cu;
+  double stage1, stage2, tile;
+};
+template <int TM, int TN, int SLOTS, int WAVES>
+constexpr KeptVariant kept_variant(int per_cu, double stage1, double stage2, double tile) {
+  return {TM, TN, SLOTS, (int)KeptGeom<TM, TN, SLOTS>::kLds, kept_gradient<TM, TN, SLOTS, WAVES>, kept_join<TM, TN>,
+          per_cu, stage1, stage2, tile};
+}
+const KeptVariant kVariants[] = {
+    kept_variant<256, 256, 3, 1>(1, 1.10, 1.10, 10.0),
+    kept_variant<128, 128, 3, 2>(2, 0.45, 0.70, 3.0),
+    kept_variant<64, 64, 4, 3>(3, 0.25, 0.45, 1.7),
+};
+int64_t tiles_of(const KeptVariant& v, int64_t out_cols, int64_t cols) {
+  return ((out_cols + v.tm - 1) / v.tm) * ((cols + v.tn - 1) / v.tn);
 }
 
 }  // namespace
@@ -223,9 +274,52 @@ hipError_t launch_checkpoint_unpack(const CheckpointArgs& a, hipStream_t stream)
   return hipGetLastError();
 }
 
-hipError_t launch_checkpoint_gradient(const CheckpointArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(checkpoint_gradient_simple, dim3((uint32_t)((a.cols + 31) / 32 * ((a.out_cols + 31) / 32))), dim3(64), 0,
-                     stream, a);
+CheckpointChoice choose_checkpoint(int64_t tokens, int64_t cols, int64_t out_cols, int es, int cu_count) {
+  CheckpointChoice best = {0, 1, 0};
+  double least = 1e300;
+  const double all = (double)((tokens + kKeptTokens - 1) / kKeptTokens), results = (double)cols * out_cols;
+  for (int i = 0; i < (int)(sizeof(kVariants) / sizeof(kVariants[0])); ++i)
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      const KeptVariant& v = kVariants[i];
+      const double tiles = (double)tiles_of(v, out_cols, cols), items = tiles * splits;
+      // (A launch holds fewer than 2^32 threads.)
+      if (splits > 1 && (all < 3 * splits || items * v.tm * v.tn * 4 > (512 << 20))) break;
+      if (items > (1 << 23) && i > 0) break;
+      const double stages = ceil(all / splits), at_once = (double)v.per_cu * cu_count;
+      const double full = floor(items / at_once), rest = items - full * at_once;
+      double t = full * (stages * v.stage2 + v.tile);
+      if (rest > 0) t += stages * (rest <= cu_count ? v.stage1 : v.stage2) + v.tile;
+      const double memory = ((double)tokens * cols + 2.0 * tokens * out_cols + es * results) / 5.0e6;
+      t = t > memory ? t : memory;
+      if (splits > 1) t += 4.0 + (2 * items * v.tm * v.tn * 4 + es * results) / 5.0e6;  // kept_join
+      if (t >= least) continue;
+      least = t;
+      best = {i, splits, splits > 1 ? (int64_t)items * v.tm * v.tn * 4 : 0};
+    }
+  return best;
+}
+
+CheckpointKernel checkpoint_kernel(int variant) {
+  const KeptVariant& v = kVariants[variant];
+  return {v.tm, v.tn, v.slots};
+}
+
+hipError_t prepare_checkpoint() {
+  for (const KeptVariant& v : kVariants) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(v.kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, v.lds);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_checkpoint_gradient(const CheckpointArgs& a, int variant, hipStream_t stream) {
+  const KeptVariant& v = kVariants[variant];
+  const int64_t tiles = tiles_of(v, a.out_cols, a.cols);
+  hipLaunchKernelGGL(v.kernel, dim3((uint32_t)(tiles * a.splits)), dim3(256), v.lds, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL(v.join, dim3((uint32_t)(tiles * (v.tm / 32) * (v.tn / 32))), dim3(64), 0, stream, a);
   return hipGetLastError();
 }
 

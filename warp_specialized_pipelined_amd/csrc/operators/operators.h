@@ -145,10 +145,24 @@ struct CheckpointArgs {
   void* dw;               // bf16 or fp32
   int64_t out_cols, dy_rs, dw_rs;
   bool fp32, accumulate;  // accumulate: dw += (fp32)
+  int32_t splits;
+  mid_piece* partials;    // workspace: the splits' sums
 };
 hipError_t launch_checkpoint_pack(const CheckpointArgs& a, hipStream_t stream);
 hipError_t launch_checkpoint_unpack(const CheckpointArgs& a, hipStream_t stream);
-hipError_t launch_checkpoint_gradient(const CheckpointArgs& a, hipStream_t stream);
+// The gradient's kernel, the ranges its tokens are split into, and the
+// workspace.  es: bytes of an element of dw.
+struct CheckpointChoice {
+  int variant, splits;
+  int64_t workspace_bytes;
+};
+CheckpointChoice choose_checkpoint(int64_t tokens, int64_t cols, int64_t out_cols, int es, int cu_count);
+struct CheckpointKernel {
+  int tile_m, tile_n, lds_stages;
+};
+CheckpointKernel checkpoint_kernel(int variant);
+hipError_t prepare_checkpoint();
+hipError_t launch_checkpoint_gradient(const CheckpointArgs& a, int variant, hipStream_t stream);
 
 // ------------------------------------------------------------------- loss
 
