@@ -177,9 +177,8 @@ __global__ __launch_bounds__(256, WAVES) void kept_gradient(CheckpointArgs a) {
   const MidTile t = mid_tile(tile, tiles_m, tiles_n);
   const int stages = (int)((a.tokens + kKeptTokens - 1) / kKeptTokens);
   const int k0 = (int)((int64_t)stages * split / a.splits), k1 = (int)((int64_t)stages * (split + 1) / a.splits);
-  const int64_t kend = (int64_t)k1 * kKeptTokens < a.tokens ? (int64_t)k1 * kKeptTokens : a.tokens;
   MidAccum<BM, BN> acc;
-  kept_loop<TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0, k1 - k0, kend);
+  kept_loop<TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0, k1 - k0);
   if (a.splits > 1) {
     mid_put(a.partials, slot, acc, wave, lane);
     return;

@@ -125,16 +125,16 @@ struct KeptLoader {
   }
 };
 
-// Stages [k0, k0 + KT) of the tile at (m0, n0); tokens past kend (at most all)
-// read as zero.  On return every wave is done with the ring.
+// Stages [k0, k0 + KT) of the tile at (m0, n0).  Tokens past the last lie past
+// dy's end, where loads give zeros, so no load needs a mask.  On return every wave is done with the ring.
 template <int TM, int TN, int SLOTS>
 __device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const CheckpointArgs& a, int64_t m0,
-                                          int64_t n0, int wave, int lane, int k0, int KT, int64_t kend) {
+                                          int64_t n0, int wave, int lane, int k0, int KT) {
   typedef KeptGeom<TM, TN, SLOTS> T;
   constexpr int BM = T::kBM, BN = T::kBN, NLA = T::kLoadsA, NLB = T::kLoadsB, P = BM * BN;
   MidLoader<2, false, NLA> la;
   KeptLoader<TN, BN, NLB> lb;
-  la.init(a.dy, a.tokens > 0 ? ((a.tokens - 1) * a.dy_rs + a.out_cols) * 2 : 0, a.dy_rs, m0, k0, kend, wave, lane);
+  la.init(a.dy, a.tokens > 0 ? ((a.tokens - 1) * a.dy_rs + a.out_cols) * 2 : 0, a.dy_rs, m0, k0, a.tokens, wave, lane);
   lb.init(a, n0, k0, wave, lane);
   KeptReader<BM> ra;
   ra.init((wave >> 1) * 32 * BM, lane);
@@ -168,7 +168,7 @@ __device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const
   };
   auto load = [&](const auto& sa, const auto& sb, auto jc, uint32_t slot) {
     constexpr int j = decltype(jc)::value;
-    if constexpr (j < NLA) la.load(sa, slot, wave, j);
+    if constexpr (j < NLA) dma16(sa.rsrc, lds_at(slot + (wave * NLA + j) * 1024), la.off[j]);
     else if constexpr (j < NLA + NLB) dma16(sb.codes, lds_at(slot + T::kCodes + (wave * NLB + j - NLA) * 1024), lb.code_off[j - NLA]);
     else dma4(sb.powers, lds_at(slot + T::kPowers + wave * 256), lb.power_off);
   };
@@ -201,8 +201,10 @@ __device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const
     static_for<0, 3 * BN + BM + BN>([&](auto xc) { prepare(std::integral_constant<int, 0>{}, xc, 0); });
     static_for<0, 3>([&](auto kc) { step(kc, 0, nothing); });
   }
+  // (The last k-step comes after the loop: a way out inside it would let the
+  // compiler move a fragment's conversion past its products.)
   uint32_t cur = 0;
-  for (int d = 0; d < KT; ++d) {
+  for (int d = 0; d + 1 < KT; ++d) {
     // Stage d + 1 has landed and this wave's reads of stage d have returned;
     // past the barrier that holds for every wave.
     sched_fence();
@@ -217,12 +219,16 @@ __device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const
       static_for<m * T::kLoads / (4 * P), (m + 1) * T::kLoads / (4 * P)>([&](auto jc) { load(sa, sb, jc, cur); });
     };
     step(std::integral_constant<int, 3>{}, nxt, [&](auto mc) { loads(std::integral_constant<int, 0>{}, mc); });
-    if (d + 1 == KT) break;
     static_for<0, 3>([&](auto kc) {
       step(kc, nxt, [&](auto mc) { loads(std::integral_constant<int, decltype(kc)::value + 1>{}, mc); });
     });
     cur = nxt;
   }
+  if (KT > 0)
+    static_for<0, P>([&](auto mc) {
+      constexpr int m = decltype(mc)::value;
+      acc.v[m / BN][m % BN] = mfma<2>(fb[1][m % BN], fa[1][m / BN], acc.v[m / BN][m % BN]);
+    });
   sched_fence();
   wait_vmcnt<0>();
   wait_lgkmcnt<0>();
