@@ -223,7 +223,7 @@ size_t gemm_quantize_workspace_size(const migemm_quantize_plan*) { return 0; }
 
 int gemm_quantize_plan_get_info(const migemm_quantize_plan* p, migemm_quantize_info* out) {
   if (!is_live(p, kQuantize) || !out) return MIGEMM_ERR_INVALID_ARG;
-  const NormShape s = norm_shape(p->desc.rows, p->desc.cols);
+  const NormShape s = quantize_shape(p->desc.rows, p->desc.cols);
   *out = {s.waves, s.vectors, p->cus};
   return MIGEMM_OK;
 }

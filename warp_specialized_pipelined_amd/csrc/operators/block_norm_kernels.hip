@@ -83,6 +83,10 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   for (int i = 0; i < NV; ++i) rv[i] = load8(r, at(i), a.cols);
 #pragma unroll
   for (int i = 0; i < NV; ++i) wv[i] = load8(w, at(i), a.cols);
+  // With one vector a lane, where a row's latency counts, w_post is on its way
+  // before the first sum, too; else it is read behind it, from the caches.
+  u32x4 early = {0, 0, 0, 0};
+  if (NV == 1 && a.post_weight) early = load8(pw, at(0), a.cols);
 
   float post = 1.0f;
   if (a.post_weight) {
@@ -99,8 +103,8 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   unsigned short* ho = static_cast<unsigned short*>(a.h) + row * a.h_rs;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    u32x4 pv;
-    if (a.post_weight) pv = load8(pw, at(i), a.cols);
+    u32x4 pv = early;
+    if (NV > 1 && a.post_weight) pv = load8(pw, at(i), a.cols);
     u32x4 o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {

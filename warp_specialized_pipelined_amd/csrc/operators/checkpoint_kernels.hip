@@ -34,44 +34,46 @@ __device__ __forceinline__ uint32_t exponent_of(uint32_t top) {
 }
 __device__ __forceinline__ float power_of(uint32_t e) { return __uint_as_float(e << 23); }
 
-// Columns a lane packs or unpacks.
-constexpr int kPackCols = 4;
-
-// A wave's item: tokens of a group x 256 columns, numbered along the columns
-// first; lane l holds columns 4 l .. 4 l + 3 of them.
+// A wave's item: tokens of a group x 64 COLS columns, numbered along the columns
+// first; lane l holds columns COLS l .. + COLS - 1 of them.
+template <int COLS>
 struct PackItem {
   int64_t group, col;
   __device__ __forceinline__ PackItem(int64_t item, int64_t ld, int lane) {
-    const int64_t across = (ld + 64 * kPackCols - 1) / (64 * kPackCols);
+    const int64_t across = (ld + 64 * COLS - 1) / (64 * COLS);
     group = item / across;
-    col = ((item - group * across) * 64 + lane) * kPackCols;
+    col = ((item - group * across) * 64 + lane) * COLS;
   }
 };
 
-// 32 tokens x 256 columns.
+// 32 tokens x 256 columns, four a lane.
+constexpr int kPackCols = 4;
+typedef uint32_t pack_words __attribute__((ext_vector_type(kPackCols / 2)));
+typedef uint32_t pack_bytes __attribute__((ext_vector_type(kPackCols / 4)));
 __device__ __forceinline__ void pack_item(const CheckpointArgs& a, int64_t item, int lane) {
-  const PackItem at(item, a.ld, lane);
+  constexpr int W = kPackCols / 2;
+  const PackItem<kPackCols> at(item, a.ld, lane);
   const int64_t c = at.col, t0 = at.group * 32;
-  if (c >= a.ld) return;
   const unsigned short* x = static_cast<const unsigned short*>(a.x) + t0 * a.x_rs + c;
-  u32x2 v[32];
+  pack_words v[32];
 #pragma unroll
   for (int t = 0; t < 32; ++t) {
-    v[t] = u32x2{0, 0};
-    if (t0 + t < a.tokens && c < a.cols) v[t] = *reinterpret_cast<const u32x2*>(x + t * a.x_rs);
+    v[t] = pack_words{};
+    if (t0 + t < a.tokens && c < a.cols) v[t] = *reinterpret_cast<const pack_words*>(x + t * a.x_rs);
   }
   // (Columns past the last: their bytes may hold anything.)
+  if (a.cols - c < kPackCols) {
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int64_t left = a.cols - c - 2 * w;
-    const uint32_t keep = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
+    for (int w = 0; w < W; ++w) {
+      const int64_t left = a.cols - c - 2 * w;
+      const uint32_t keep = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
 #pragma unroll
-    for (int t = 0; t < 32; ++t) v[t][w] &= keep;
+      for (int t = 0; t < 32; ++t) v[t][w] &= keep;
+    }
   }
-  unsigned char* codes = a.codes + (t0 / 16) * a.ld * 16 + c * 16;
-  uint32_t exponents = 0;
+  uint32_t exponents[kPackCols];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
+  for (int w = 0; w < W; ++w) {
     uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < 32; ++t) top = max_u16x2(top, v[t][w] & 0x7FFF7FFFu);
@@ -81,42 +83,64 @@ __device__ __forceinline__ void pack_item(const CheckpointArgs& a, int64_t item,
       top = 0;
 #pragma unroll
       for (int t = 0; t < 32; ++t) {
-        uint32_t m = v[t][w] & 0x7FFF7FFFu, s = v[t][w] & 0x80008000u, o = 0;
+        const uint32_t m = v[t][w] & 0x7FFF7FFFu;
+        uint32_t o = 0, f = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t b = (m >> (16 * h)) & 0xFFFFu;
-          if (b >= 0x7F80u) b = 0x7FC0u;
-          else if (b > 0x7F60u) b = 0x7F60u;
+          b = b >= 0x7F80u ? 0x7FC0u : (b > 0x7F60u ? 0x7F60u : b);
           o |= b << (16 * h);
+          f |= (b >= 0x7F80u ? 0u : b) << (16 * h);
         }
-        v[t][w] = o | s;
-        const uint32_t f = ((o & 0xFFFFu) >= 0x7F80u ? 0 : o & 0xFFFFu) | ((o >> 16) >= 0x7F80u ? 0 : o & 0xFFFF0000u);
+        v[t][w] = o | (v[t][w] & 0x80008000u);
         top = max_u16x2(top, f);
       }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t e = exponent_of(h ? top >> 16 : top & 0xFFFFu);
-      exponents |= e << (8 * (2 * w + h));
-      const float scale = power_of(e);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        u32x4 o;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          i16x2 d = {0, 0};
-          const int t = 16 * g + 4 * q;
-          const uint32_t p0 = __builtin_amdgcn_perm(v[t + 1][w], v[t][w], h ? 0x07060302u : 0x05040100u);
-          const uint32_t p1 = __builtin_amdgcn_perm(v[t + 3][w], v[t + 2][w], h ? 0x07060302u : 0x05040100u);
-          d = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(d, __builtin_bit_cast(bf16x2, p0), scale, false);
-          d = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(d, __builtin_bit_cast(bf16x2, p1), scale, true);
-          o[q] = __builtin_bit_cast(uint32_t, d);
-        }
-        *reinterpret_cast<u32x4*>(codes + g * a.ld * 16 + (2 * w + h) * 16) = o;
-      }
-    }
+    exponents[2 * w] = exponent_of(top & 0xFFFFu);
+    exponents[2 * w + 1] = exponent_of(top >> 16);
   }
-  *reinterpret_cast<uint32_t*>(a.scales + at.group * a.ld + c) = exponents;
+  // A lane's chunks (16 tokens of a column) go through LDS, so that the stores of
+  // a wave are whole lines: chunk h of lane l is at C l + (h + l / (16 / C)) % C,
+  // which spreads 16 lanes over all banks both when it is written and when lane
+  // i reads column 64 s + i.
+  constexpr int C = kPackCols;
+  __shared__ u32x4 chunks[64 * C];
+  auto place = [](int l, int h) { return C * l + ((h + l / (16 / C)) & (C - 1)); };
+  const int64_t first = c - C * lane;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    if (g > 0) __syncthreads();
+#pragma unroll
+    for (int h = 0; h < C; ++h) {
+      const float scale = power_of(exponents[h]);
+      const uint32_t sel = h & 1 ? 0x07060302u : 0x05040100u;
+      u32x4 o;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int t = 16 * g + 4 * q;
+        const uint32_t p0 = __builtin_amdgcn_perm(v[t + 1][h / 2], v[t][h / 2], sel);
+        const uint32_t p1 = __builtin_amdgcn_perm(v[t + 3][h / 2], v[t + 2][h / 2], sel);
+        i16x2 d = {0, 0};
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(d, __builtin_bit_cast(bf16x2, p0), scale, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(d, __builtin_bit_cast(bf16x2, p1), scale, true);
+        o[q] = __builtin_bit_cast(uint32_t, d);
+      }
+      chunks[place(lane, h)] = o;
+    }
+    __syncthreads();
+    u32x4* codes = reinterpret_cast<u32x4*>(a.codes) + (t0 / 16 + g) * a.ld + first;
+#pragma unroll
+    for (int s = 0; s < C; ++s)
+      if (first + 64 * s + lane < a.ld) codes[64 * s + lane] = chunks[place((64 * s + lane) / C, lane & (C - 1))];
+  }
+  __syncthreads();
+  if (c < a.ld) {
+    pack_bytes e;
+#pragma unroll
+    for (int w = 0; w < C / 4; ++w)
+      e[w] = exponents[4 * w] | exponents[4 * w + 1] << 8 | exponents[4 * w + 2] << 16 | exponents[4 * w + 3] << 24;
+    *reinterpret_cast<pack_bytes*>(a.scales + at.group * a.ld + c) = e;
+  }
 }
 __global__ __launch_bounds__(64) void checkpoint_pack(CheckpointArgs a, int64_t items) {
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) pack_item(a, i, threadIdx.x);
@@ -127,23 +151,24 @@ __device__ __forceinline__ uint32_t two_bf16(uint32_t codes, float scale, bool u
                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false));
 }
 
-// 16 tokens x 256 columns.
+// 16 tokens x 256 columns, four a lane.
+constexpr int kUnpackCols = 4;
 __device__ __forceinline__ void unpack_item(const CheckpointArgs& a, int64_t item, int lane) {
-  const PackItem at(item, a.ld, lane);
+  const PackItem<kUnpackCols> at(item, a.ld, lane);
   const int64_t c = at.col, t0 = at.group * 16;
   if (c >= a.cols) return;
   const u32x4* codes = reinterpret_cast<const u32x4*>(a.codes) + at.group * a.ld + c;
   const uint32_t exponents = *reinterpret_cast<const uint32_t*>(a.scales + (at.group / 2) * a.ld + c);
-  u32x4 v[kPackCols];
+  u32x4 v[kUnpackCols];
 #pragma unroll
-  for (int i = 0; i < kPackCols; ++i) v[i] = codes[i];
+  for (int i = 0; i < kUnpackCols; ++i) v[i] = codes[i];
   unsigned short* x = static_cast<unsigned short*>(a.x_out) + t0 * a.x_rs + c;
   const int64_t left = a.cols - c;
 #pragma unroll
   for (int t = 0; t < 16; t += 2) {
-    uint32_t p[kPackCols];  // tokens t and t + 1 of a column
+    uint32_t p[kUnpackCols];  // tokens t and t + 1 of a column
 #pragma unroll
-    for (int i = 0; i < kPackCols; ++i)
+    for (int i = 0; i < kUnpackCols; ++i)
       p[i] = two_bf16(v[i][t >> 2], power_of((exponents >> (8 * i)) & 0xFFu), t & 2);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -249,6 +274,8 @@ constexpr KeptVariant kept_variant(int per_cu, double stage1, double stage2, dou
 }
 const KeptVariant kVariants[] = {
     kept_variant<256, 256, 3, 1>(1, 1.10, 1.10, 10.0),
+    kept_variant<192, 256, 3, 1>(1, 0.95, 0.95, 8.0),
+    kept_variant<128, 256, 3, 1>(1, 0.70, 0.70, 6.0),
     kept_variant<128, 128, 3, 2>(2, 0.45, 0.70, 3.0),
     kept_variant<64, 64, 4, 3>(3, 0.25, 0.45, 1.7),
 };
@@ -262,13 +289,13 @@ int64_t tiles_of(const KeptVariant& v, int64_t out_cols, int64_t cols) {
 static uint32_t wave_grid(int64_t items) { return (uint32_t)(items < (1 << 25) ? items : 1 << 25); }
 
 hipError_t launch_checkpoint_pack(const CheckpointArgs& a, hipStream_t stream) {
-  const int64_t items = (a.tokens + 31) / 32 * ((a.ld + 255) / 256);
+  const int64_t items = (a.tokens + 31) / 32 * ((a.ld + 64 * kPackCols - 1) / (64 * kPackCols));
   hipLaunchKernelGGL(checkpoint_pack, dim3(wave_grid(items)), dim3(64), 0, stream, a, items);
   return hipGetLastError();
 }
 
 hipError_t launch_checkpoint_unpack(const CheckpointArgs& a, hipStream_t stream) {
-  const int64_t items = (a.tokens + 15) / 16 * ((a.ld + 255) / 256);
+  const int64_t items = (a.tokens + 15) / 16 * ((a.ld + 64 * kUnpackCols - 1) / (64 * kUnpackCols));
   hipLaunchKernelGGL(checkpoint_unpack, dim3(wave_grid(items)), dim3(64), 0, stream, a, items);
   return hipGetLastError();
 }

@@ -87,6 +87,36 @@ __device__ __forceinline__ bf16x8 kept_bf16(int w0, int w1, float power) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// dy's loads of a stage: MidLoader's layout, for any whole number of loads a
+// wave.  Tokens past the last lie past dy's end, where loads give zeros, so no
+// load needs a mask.
+template <int NL>
+struct KeptDyLoader {
+  typedef StageGeom<2> G;
+  uint64_t at;  // the next stage's
+  int64_t left, step;
+  uint32_t off[NL];
+  __device__ __forceinline__ void init(const CheckpointArgs& a, int64_t m0, int stage, int wave, int lane) {
+    step = (int64_t)kKeptTokens * a.dy_rs * 2;
+    at = reinterpret_cast<uint64_t>(a.dy) + m0 * 2 + stage * step;
+    // (Range checks work on dwords: up to the end of the last 16-byte block.)
+    left = (((a.tokens - 1) * a.dy_rs + a.out_cols - m0) * 2 - stage * step + 15) & ~(int64_t)15;
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+      const int idx = wave * NL + j;  // 8 rows of a panel
+      const int row = (idx % G::kLoadsPerPanel) * 8 + (lane >> 3);
+      const int col = (idx / G::kLoadsPerPanel) * G::kPanelCols + ((lane & 7) ^ swz_mn<2>(row)) * G::kElemsPerChunk;
+      off[j] = (uint32_t)((row * a.dy_rs + col) * 2);
+    }
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t next() {
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(reinterpret_cast<const void*>(at), left < 0 ? 0 : (left > 0x7FFFFFF0 ? 0x7FFFFFF0u : (uint32_t)left));
+    at += step, left -= step;
+    return r;
+  }
+};
+
 // The codes' and powers' loads of a stage.  Groups of tokens past the kept ones
 // read as zero; columns past the last read other codes, or zeros, for columns
 // of dw that are not stored.
@@ -125,16 +155,17 @@ struct KeptLoader {
   }
 };
 
-// Stages [k0, k0 + KT) of the tile at (m0, n0).  Tokens past the last lie past
-// dy's end, where loads give zeros, so no load needs a mask.  On return every wave is done with the ring.
-template <int TM, int TN, int SLOTS>
-__device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const CheckpointArgs& a, int64_t m0,
-                                          int64_t n0, int wave, int lane, int k0, int KT) {
+// Stages [k0, k0 + KT) of the tile at (m0, n0).  On return every wave is done with the ring.
+// WAVE: the wave, as a constant: each issues its loads at its own products.
+template <int TM, int TN, int SLOTS, int WAVE>
+__device__ __forceinline__ void kept_loop_of(MidAccum<TM / 64, TN / 64>& acc, const CheckpointArgs& a, int64_t m0,
+                                             int64_t n0, int lane, int k0, int KT) {
+  constexpr int wave = WAVE;
   typedef KeptGeom<TM, TN, SLOTS> T;
   constexpr int BM = T::kBM, BN = T::kBN, NLA = T::kLoadsA, NLB = T::kLoadsB, P = BM * BN;
-  MidLoader<2, false, NLA> la;
+  KeptDyLoader<NLA> la;
   KeptLoader<TN, BN, NLB> lb;
-  la.init(a.dy, a.tokens > 0 ? ((a.tokens - 1) * a.dy_rs + a.out_cols) * 2 : 0, a.dy_rs, m0, k0, a.tokens, wave, lane);
+  la.init(a, m0, k0, wave, lane);
   lb.init(a, n0, k0, wave, lane);
   KeptReader<BM> ra;
   ra.init((wave >> 1) * 32 * BM, lane);
@@ -168,7 +199,7 @@ __device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const
   };
   auto load = [&](const auto& sa, const auto& sb, auto jc, uint32_t slot) {
     constexpr int j = decltype(jc)::value;
-    if constexpr (j < NLA) dma16(sa.rsrc, lds_at(slot + (wave * NLA + j) * 1024), la.off[j]);
+    if constexpr (j < NLA) dma16(sa, lds_at(slot + (wave * NLA + j) * 1024), la.off[j]);
     else if constexpr (j < NLA + NLB) dma16(sb.codes, lds_at(slot + T::kCodes + (wave * NLB + j - NLA) * 1024), lb.code_off[j - NLA]);
     else dma4(sb.powers, lds_at(slot + T::kPowers + wave * 256), lb.power_off);
   };
@@ -216,7 +247,10 @@ __device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const
     const auto sb = lb.next();
     auto loads = [&](auto first, auto mc) {
       constexpr int m = decltype(first)::value * P + decltype(mc)::value;
-      static_for<m * T::kLoads / (4 * P), (m + 1) * T::kLoads / (4 * P)>([&](auto jc) { load(sa, sb, jc, cur); });
+      // Load j stands behind product (j + wave / 4) 4 P / kLoads of the stage's 4 P.
+      static_for<0, T::kLoads>([&](auto jc) {
+        if constexpr ((4 * decltype(jc)::value + WAVE) * P / T::kLoads == m) load(sa, sb, jc, cur);
+      });
     };
     step(std::integral_constant<int, 3>{}, nxt, [&](auto mc) { loads(std::integral_constant<int, 0>{}, mc); });
     static_for<0, 3>([&](auto kc) {
@@ -233,6 +267,15 @@ __device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const
   wait_vmcnt<0>();
   wait_lgkmcnt<0>();
   barrier();
+}
+
+template <int TM, int TN, int SLOTS>
+__device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const CheckpointArgs& a, int64_t m0,
+                                          int64_t n0, int wave, int lane, int k0, int KT) {
+  if (wave == 0) kept_loop_of<TM, TN, SLOTS, 0>(acc, a, m0, n0, lane, k0, KT);
+  else if (wave == 1) kept_loop_of<TM, TN, SLOTS, 1>(acc, a, m0, n0, lane, k0, KT);
+  else if (wave == 2) kept_loop_of<TM, TN, SLOTS, 2>(acc, a, m0, n0, lane, k0, KT);
+  else kept_loop_of<TM, TN, SLOTS, 3>(acc, a, m0, n0, lane, k0, KT);
 }
 
 // The wave's part of the tile in fp32, 32 rows at a time staged through LDS

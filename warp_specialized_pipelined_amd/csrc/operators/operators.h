@@ -54,6 +54,7 @@ struct QuantizeArgs {
   int64_t rows, cols;
   int64_t x_rs, q_rs;  // elements
 };
+NormShape quantize_shape(int64_t rows, int64_t cols);
 hipError_t launch_quantize(const QuantizeArgs& a, bool e4m3, hipStream_t stream);
 
 // ------------------------------------------------------------- block norm

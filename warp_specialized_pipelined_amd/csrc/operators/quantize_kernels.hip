@@ -94,13 +94,21 @@ quantize_fn pick(int nv) {
 }
 template <bool E4M3>
 quantize_fn pick_shape(NormShape s) {
+  if (s.vectors == 8) return quantize_rows<4, 8, E4M3>;
   return s.waves == 1 ? pick<1, E4M3>(s.vectors) : (s.waves == 4 ? pick<4, E4M3>(s.vectors) : pick<16, E4M3>(s.vectors));
 }
 
 }  // namespace
 
+// The norm's shapes, but many rows of 8193 to 16384 columns are shared by four
+// waves with eight vectors a lane.
+NormShape quantize_shape(int64_t rows, int64_t cols) {
+  const NormShape s = norm_shape(rows, cols);
+  return rows > 256 && s.waves == 16 && s.vectors <= 2 ? NormShape{4, 8} : s;
+}
+
 hipError_t launch_quantize(const QuantizeArgs& a, bool e4m3, hipStream_t stream) {
-  const NormShape s = norm_shape(a.rows, a.cols);
+  const NormShape s = quantize_shape(a.rows, a.cols);
   const quantize_fn f = e4m3 ? pick_shape<true>(s) : pick_shape<false>(s);
   int64_t grid = (a.rows + rows_of(s.waves) - 1) / rows_of(s.waves);
   if (grid > (1 << 20)) grid = 1 << 20;  // a launch holds fewer than 2^32 threads
