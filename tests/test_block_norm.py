@@ -476,13 +476,22 @@ def test_runs_agree_on_streams_and_in_a_graph(y_type):
 
 
 @pytest.mark.gpu
-def test_kernels_that_a_plan_chooses():
-    for rows, cols, shape in ((1, 512, (1, 1)), (2000, 1000, (1, 2)), (2000, 2000, (1, 4)), (5, 2048, (4, 1)),
-                              (300, 4000, (4, 2)), (300, 8192, (4, 4)), (3, 8000, (16, 1)), (300, 16000, (16, 2))):
-        p = Block(rows, cols)
+@pytest.mark.parametrize("rows,cols,forward,backward", [
+    (5, 512, (1, 1), (1, 1)), (2000, 500, (1, 1), (1, 1)), (300, 1001, (1, 2), (1, 2)), (300, 2000, (1, 4), (4, 1)),
+    (5, 2048, (4, 1), (4, 1)), (300, 4001, (4, 2), (4, 2)), (300, 8190, (4, 4), (8, 2)), (3, 8001, (16, 1), (16, 1)),
+    (40, 16383, (8, 4), (8, 4)), (700, 12001, (8, 4), (8, 4))])
+def test_kernels_that_a_plan_chooses(rows, cols, forward, backward):
+    for gate, post in ((True, True), (False, True), (True, False), (False, False)):
+        p = Block(rows, cols, post=post, gate=gate, seed=rows + cols)
         i = p.plan.info
-        assert (i.forward_waves, i.forward_vectors) == (i.backward_waves, i.backward_vectors) == shape
-        assert i.backward_workgroups * cols * 2 * 4 == p.plan.workspace_size
+        assert (i.forward_waves, i.forward_vectors) == forward and (i.backward_waves, i.backward_vectors) == backward
+        assert i.backward_workgroups * cols * (1 + post) * 4 == p.plan.workspace_size
+        p.forward()
+        p.backward()
+        torch.cuda.synchronize()
+        check(p)
+        check_backward(p)
+        untouched(p)
 
 
 @pytest.mark.gpu

@@ -250,14 +250,14 @@ int gemm_block_norm_plan_create(const migemm_block_norm_desc* desc, migemm_block
   if (st != MIGEMM_OK) return st;
   int cus = 0;
   static std::atomic<bool> prepared[kMaxDevices];
-  st = check_device(desc->device, &cus, prepared, nothing);
+  st = check_device(desc->device, &cus, prepared, prepare_block_norm);
   if (st != MIGEMM_OK) return st;
   migemm_block_norm_plan* p = new (std::nothrow) migemm_block_norm_plan();
   if (!p) return MIGEMM_ERR_INVALID_ARG;
   p->desc = *desc;
   p->cus = cus;
   if (with_backward(*desc)) {
-    p->partial_rows = norm_partial_rows(desc->rows, desc->cols, cus);
+    p->partial_rows = block_norm_partial_rows(desc->rows, desc->cols, cus);
     p->workspace_bytes = (size_t)(p->partial_rows * desc->cols * (desc->post_norm ? 2 : 1) * 4);
   }
   return add_live(p, kBlockNorm, out);
@@ -271,9 +271,10 @@ size_t gemm_block_norm_workspace_size(const migemm_block_norm_plan* plan) {
 
 int gemm_block_norm_plan_get_info(const migemm_block_norm_plan* p, migemm_block_norm_info* out) {
   if (!is_live(p, kBlockNorm) || !out) return MIGEMM_ERR_INVALID_ARG;
-  const NormShape f = norm_shape(p->desc.rows, p->desc.cols);
+  const NormShape f = block_norm_forward_shape(p->desc.rows, p->desc.cols);
+  const NormShape b = block_norm_backward_shape(p->desc.rows, p->desc.cols);
   const bool back = with_backward(p->desc);
-  *out = {f.waves, f.vectors, back ? f.waves : 0, back ? f.vectors : 0, (int32_t)p->partial_rows, p->cus};
+  *out = {f.waves, f.vectors, back ? b.waves : 0, back ? b.vectors : 0, (int32_t)p->partial_rows, p->cus};
   return MIGEMM_OK;
 }
 

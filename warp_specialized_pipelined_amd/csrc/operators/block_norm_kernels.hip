@@ -36,11 +36,23 @@ __device__ __forceinline__ float element(const u32x4& v, int e) { return e & 1 ?
 struct Gate {
   float s, ds;
   __device__ __forceinline__ explicit Gate(float z) {
-    const float e = __builtin_amdgcn_exp2f(-fabsf(z) * 1.4426950408889634f), r = 1.0f / (1.0f + e);
+    const float e = __builtin_amdgcn_exp2f(-fabsf(z) * 1.4426950408889634f), r = __builtin_amdgcn_rcpf(1.0f + e);
     s = z < 0.0f ? e * r : r;
     ds = e * r * r;
   }
 };
+
+// Values the compiler cannot see through: what was unpacked from them before
+// is unpacked again where it is needed, instead of being held in registers
+// twice as wide across a reduction (which did not fit: 8192 x 8192 backward
+// took 998 us with spilled registers).
+template <int N>
+__device__ __forceinline__ void hide(u32x4 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
+__device__ __forceinline__ void apart() { __builtin_amdgcn_sched_barrier(0); }
 
 // The sum over the row of every lane's v, given to all of them: WAVES waves
 // share the row, `buffer` holds a sum of each.
@@ -65,28 +77,22 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   // ones, and cannot come round to these before a barrier between.
   __shared__ float posts[2][WAVES], sums[2][WAVES];
   __shared__ uint32_t tops[2][WAVES];
-  const auto row_of = [&](const void* m, int64_t rs) { return static_cast<const unsigned short*>(m) + row * rs; };
-  const auto at = [&](int i) { return (int64_t)(i * kLanes + t) * 8; };
-  const unsigned short* x = row_of(a.x, a.x_rs);
-  const unsigned short* r = row_of(a.r, a.r_rs);
-  const unsigned short* w = static_cast<const unsigned short*>(a.weight);
-  const unsigned short* pw = static_cast<const unsigned short*>(a.post_weight);
+  const auto at = [&](int i) { return (i * kLanes + t) * 8; };
+  const auto load = [&](u32x4 (&v)[NV], const void* m, int64_t rs) {
+    const RowView from = RowView::in(m, row * rs, a.cols);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = from.load(at(i));
+  };
+  const RowView pw = RowView::in(a.post_weight, 0, a.post_weight ? a.cols : 0);
   u32x4 xv[NV], rv[NV], zv[NV], wv[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) xv[i] = load8(x, at(i), a.cols);
-  if constexpr (GATE) {
-    const unsigned short* z = row_of(a.z, a.z_rs);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) zv[i] = load8(z, at(i), a.cols);
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) rv[i] = load8(r, at(i), a.cols);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) wv[i] = load8(w, at(i), a.cols);
+  load(xv, a.x, a.x_rs);
+  if constexpr (GATE) load(zv, a.z, a.z_rs);
+  load(rv, a.r, a.r_rs);
+  load(wv, a.weight, 0);
   // With one vector a lane, where a row's latency counts, w_post is on its way
   // before the first sum, too; else it is read behind it, from the caches.
   u32x4 early = {0, 0, 0, 0};
-  if (NV == 1 && a.post_weight) early = load8(pw, at(0), a.cols);
+  if (NV == 1 && a.post_weight) early = pw.load(at(0));
 
   float post = 1.0f;
   if (a.post_weight) {
@@ -100,11 +106,11 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   }
   float h[NV][8], sum = 0.0f;
   uint32_t top = 0;
-  unsigned short* ho = static_cast<unsigned short*>(a.h) + row * a.h_rs;
+  const RowView ho = RowView::out<2>(a.h, row * a.h_rs, a.cols);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     u32x4 pv = early;
-    if (NV > 1 && a.post_weight) pv = load8(pw, at(i), a.cols);
+    if (NV > 1 && a.post_weight) pv = pw.load(at(i));
     u32x4 o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -121,7 +127,7 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(h[i][2 * q], h[i][2 * q + 1]);
-    store8(ho, at(i), a.cols, o);
+    ho.store(at(i), o);
   }
   if constexpr (Y != kRowBf16) {
     top = wave_max_bits(top);
@@ -130,14 +136,14 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   const float rstd = rsqrtf(row_sum<WAVES>(sum, sums[phase], wave, lane) / (float)a.cols + a.eps);
   if (t == 0) a.rstd[row] = rstd;
   if constexpr (Y == kRowBf16) {
-    unsigned short* y = static_cast<unsigned short*>(a.y) + row * a.y_rs;
+    const RowView y = RowView::out<2>(a.y, row * a.y_rs, a.cols);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       u32x4 o;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         o[q] = pack_bf16x2(h[i][2 * q] * rstd * lo(wv[i][q]), h[i][2 * q + 1] * rstd * hi(wv[i][q]));
-      store8(y, at(i), a.cols, o);
+      y.store(at(i), o);
     }
   } else {
     if constexpr (WAVES > 1) {
@@ -153,7 +159,7 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
     // Rows of values so small that kTop / largest would overflow are lifted.
     const float lift = largest < 0x1p-96f ? 0x1p96f : 1.0f;
     const float inv = largest == 0.0f ? 0.0f : kTop / (largest * lift);
-    unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.y_rs;
+    const RowView y = RowView::out<1>(a.y, row * a.y_rs, a.cols);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float v[8];
@@ -166,14 +172,14 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
         o = {pack_i8x4(v[0], v[1], v[2], v[3]), pack_i8x4(v[4], v[5], v[6], v[7])};
         if (!finite) o = u32x2{0, 0};
       }
-      store8_bytes(y, at(i), a.cols, o);
+      y.store_bytes(at(i), o);
     }
   }
 }
 
 template <int WAVES, int NV, bool GATE, RowType Y>
 __global__ __launch_bounds__(threads_of(WAVES)) void block_norm_forward(BlockNormArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int t = WAVES == 1 ? lane : (int)threadIdx.x;
   int phase = 0;
   const int64_t step = (int64_t)gridDim.x * rows_of(WAVES);
@@ -182,157 +188,213 @@ __global__ __launch_bounds__(threads_of(WAVES)) void block_norm_forward(BlockNor
     block_norm_row<WAVES, NV, GATE, Y>(a, row, t, wave, lane, phase);
 }
 
-// The workgroup's sums of its columns go to its row of the workspace (dw's,
-// then dw_post's); block_norm_sum_partials adds those rows in a fixed order.
-// One workgroup alone writes the gradients itself.
-template <int WAVES, int NV>
-__device__ __forceinline__ void put_sums(const BlockNormArgs& a, const float (&dw)[NV][8], float* p, int t, int wave,
-                                         int lane) {
-  constexpr int kLanes = 64 * WAVES;
-  if constexpr (WAVES == 1) {
-    __shared__ float all[4][NV * 512];
-    __syncthreads();
+// What a lane holds of a row: the gradients that come in, h as it was stored,
+// and the block's output and its gate.
+template <int NV, bool GATE, bool POST>
+struct BackwardRow {
+  u32x4 g[NV], h[NV], d[NV], x[GATE || POST ? NV : 1], z[GATE ? NV : 1];
+  float rstd, post;
+  // (A row past the last: zeros, and nothing is read.)
+  template <class At>
+  __device__ __forceinline__ void load(const BlockNormArgs& a, int64_t row, At&& at) {
+    const bool in = row < a.rows;
+    const auto all = [&](u32x4* v, const void* m, int64_t rs) {
+      const RowView from = RowView::in(m, row * rs, in && m ? a.cols : 0);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) all[wave][(i * 64 + lane) * 8 + e] = dw[i][e];
-    __syncthreads();
-    for (int64_t c = threadIdx.x; c < a.cols; c += 256) p[c] = ((all[0][c] + all[1][c]) + all[2][c]) + all[3][c];
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(i * kLanes + t) * 8;
-      if (c + 8 <= a.cols) {
-        // (16-byte stores, which need an address that is a multiple of 4.)
-        typedef float f32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
-        *reinterpret_cast<f32x4_4*>(p + c) = f32x4_4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
-        *reinterpret_cast<f32x4_4*>(p + c + 4) = f32x4_4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < a.cols) p[c + e] = dw[i][e];
-      }
-    }
+      for (int i = 0; i < NV; ++i) v[i] = from.load(at(i));
+    };
+    all(g, a.dy, a.dy_rs);
+    all(h, a.h, a.h_rs);
+    all(d, a.dh, a.dh_rs);
+    if constexpr (GATE || POST) all(x, a.x, a.x_rs);
+    if constexpr (GATE) all(z, a.z, a.z_rs);
+    rstd = in ? a.rstd[row] : 0.0f;
+    post = POST && in ? a.post_rstd[row] : 1.0f;
   }
-}
+};
 
 // Each walker (a workgroup, or with WAVES = 1 a wave) takes rows walker,
-// walker + walkers, ... and keeps its columns' sums in registers.
-template <int WAVES, int NV, bool GATE, bool POST>
+// walker + walkers, ..., the next one on its way while a row is worked on (not
+// with 16 waves, which come with few rows and half the registers), and adds up
+// its columns' sums: in registers, or, with WIDE, where those would not
+// hold them beside four vectors of a row, in LDS (each lane its own columns).
+// The workgroup's sums go to its row of the workspace (dw's, then dw_post's);
+// block_norm_sum_partials adds those rows in a fixed order.  One workgroup alone
+// writes the gradients itself.
+template <int WAVES, int NV, bool GATE, bool POST, bool WIDE>
 __global__ __launch_bounds__(threads_of(WAVES), WAVES == 16 ? 4 : 2) void block_norm_backward(BlockNormArgs a) {
   constexpr int kLanes = 64 * WAVES;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  static_assert(!WIDE || WAVES > 1, "a wave's own sums stay in registers");
+  // (WIDE: the weights are read again for each row, from the caches.)
+  constexpr bool kReload = WIDE, kAhead = WAVES < 16;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int64_t walker = (int64_t)blockIdx.x * rows_of(WAVES) + (WAVES == 1 ? wave : 0);
   const int64_t walkers = (int64_t)gridDim.x * rows_of(WAVES);
   const int t = WAVES == 1 ? lane : (int)threadIdx.x;
-  const unsigned short* w = static_cast<const unsigned short*>(a.weight);
-  const unsigned short* pw = static_cast<const unsigned short*>(a.post_weight);
   const float cols = (float)a.cols;
-  const auto at = [&](int i) { return (int64_t)(i * kLanes + t) * 8; };
+  const auto at = [&](int i) { return (i * kLanes + t) * 8; };
   __shared__ float sums[2][WAVES], posts[2][WAVES];
+  // WIDE: [dw, dw_post][vector][half][lane], 16 bytes each.
+  f32x4* lds = WIDE ? (f32x4*)lds_at(0) : nullptr;
+  const auto slot = [&](int which, int i, int half) { return ((which * NV + i) * 2 + half) * kLanes + t; };
 
+  const RowView w = RowView::in(a.weight, 0, a.cols), pw = RowView::in(a.post_weight, 0, POST ? a.cols : 0);
   u32x4 wv[NV], pv[POST ? NV : 1];
-  float dw[NV][8], dpw[POST ? NV : 1][8];
+  float dw[WIDE ? 1 : NV][8], dpw[POST && !WIDE ? NV : 1][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    wv[i] = load8(w, at(i), a.cols);
-    if constexpr (POST) pv[i] = load8(pw, at(i), a.cols);
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dw[i][e] = 0.0f;
-      if constexpr (POST) dpw[i][e] = 0.0f;
-    }
-  }
-  int phase = 0;
-  for (int64_t row = walker; row < a.rows; row += walkers, phase ^= 1) {
-    const auto row_of = [&](const void* m, int64_t rs) { return static_cast<const unsigned short*>(m) + row * rs; };
-    const auto load = [&](u32x4 (&v)[NV], const void* m, int64_t rs) {
-      const unsigned short* p = row_of(m, rs);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = load8(p, at(i), a.cols);
-    };
-    u32x4 gv[NV], hv[NV], dv[NV], xv[NV], zv[NV];
-    load(gv, a.dy, a.dy_rs);
-    load(hv, a.h, a.h_rs);
-    if (a.dh) {
-      load(dv, a.dh, a.dh_rs);
+      for (int k = 0; k < (POST ? 4 : 2); ++k) lds[slot(k / 2, i, k % 2)] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) dv[i] = u32x4{0, 0, 0, 0};
-    }
-    if constexpr (GATE || POST) load(xv, a.x, a.x_rs);
-    if constexpr (GATE) load(zv, a.z, a.z_rs);
-    const float rstd = a.rstd[row], post = POST ? a.post_rstd[row] : 1.0f;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
+      if constexpr (!kReload) wv[i] = w.load(at(i));
+      if constexpr (POST && !kReload) pv[i] = pw.load(at(i));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float n = element(hv[i], e) * rstd, g = element(gv[i], e);
-        dw[i][e] += g * n;
-        s += g * element(wv[i], e) * n;
+        dw[i][e] = 0.0f;
+        if constexpr (POST) dpw[i][e] = 0.0f;
       }
+    }
+  }
+  BackwardRow<NV, GATE, POST> c, next;
+  if constexpr (kAhead) next.load(a, walker, at);
+  int phase = 0;
+  for (int64_t row = walker; row < a.rows; row += walkers, phase ^= 1) {
+    if constexpr (kAhead) c = next;
+    else c.load(a, row, at);
+    if constexpr (kAhead && !WIDE) next.load(a, row + walkers, at);
+    // (Pairs of elements are kept apart: all of a row's at once would not fit the
+    // registers.)
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (kReload) wv[i] = w.load(at(i));
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e % 2 == 0) apart();
+        const float n = element(c.h[i], e) * c.rstd, g = element(c.g[i], e);
+        f[e] = g * n;
+        s += g * element(wv[i], e) * n;
+        if constexpr (!WIDE) dw[i][e] += f[e];
+      }
+      if constexpr (WIDE) {
+        lds[slot(0, i, 0)] += f32x4{f[0], f[1], f[2], f[3]};
+        lds[slot(0, i, 1)] += f32x4{f[4], f[5], f[6], f[7]};
+      }
+    }
     const float mean = row_sum<WAVES>(s, sums[phase], wave, lane) / cols;
-    unsigned short* dr = static_cast<unsigned short*>(a.dr) + row * a.dr_rs;
-    unsigned short* dz = static_cast<unsigned short*>(a.dz) + row * a.dz_rs;
-    unsigned short* dx = static_cast<unsigned short*>(a.dx) + row * a.dx_rs;
-    // v of the row, in fp32, over what is needed of it no more.
+    hide(c.g);
+    hide(c.h);
+    hide(wv);
+    if constexpr (POST && !kReload) hide(pv);
+    const RowView dr = RowView::out<2>(a.dr, row * a.dr_rs, a.cols);
+    const RowView dz = RowView::out<2>(a.dz, row * a.dz_rs, a.cols);
+    const RowView dx = RowView::out<2>(a.dx, row * a.dx_rs, a.cols);
     float v[NV][8];
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      if constexpr (POST && kReload) pv[i] = pw.load(at(i));
       u32x4 o, oz;
       float f[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = element(hv[i], e) * rstd;
-        const float d = element(dv[i], e) + rstd * (element(gv[i], e) * element(wv[i], e) - n * mean);
-        f[e] = a.residual * d;
-        v[i][e] = a.branch * d;
-      }
+      for (int q = 0; q < 4; ++q) {
+        apart();
+        float r[2], z[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
-      store8(dr, at(i), a.cols, o);
-      if constexpr (GATE) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const Gate gate(element(zv[i], e));
-          float u = element(xv[i], e);
-          if constexpr (POST) u = u * post * element(pv[i], e);
-          f[e] = v[i][e] * u * gate.ds;
-          v[i][e] *= gate.s;
+        for (int k = 0; k < 2; ++k) {
+          const int e = 2 * q + k;
+          const float n = element(c.h[i], e) * c.rstd;
+          const float d = element(c.d[i], e) + c.rstd * (element(c.g[i], e) * element(wv[i], e) - n * mean);
+          r[k] = a.residual * d;
+          float g = a.branch * d;
+          const float p = GATE || POST ? element(c.x[i], e) * c.post : 0.0f;
+          const float pw_e = POST ? element(pv[i], e) : 1.0f;
+          if constexpr (GATE) {
+            const Gate gate(element(c.z[i], e));
+            z[k] = g * (p * pw_e) * gate.ds;
+            g *= gate.s;
+          }
+          if constexpr (POST) {
+            f[e] = g * p;
+            if constexpr (!WIDE) dpw[i][e] += f[e];
+            g *= pw_e;
+            s += g * p;
+          }
+          v[i][e] = g;
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) oz[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
-        store8(dz, at(i), a.cols, oz);
+        o[q] = pack_bf16x2(r[0], r[1]);
+        if constexpr (GATE) oz[q] = pack_bf16x2(z[0], z[1]);
       }
-      if constexpr (POST) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float p = element(xv[i], e) * post;
-          dpw[i][e] += v[i][e] * p;
-          v[i][e] *= element(pv[i], e);
-          s += v[i][e] * p;
-        }
+      dr.store(at(i), o);
+      if constexpr (GATE) dz.store(at(i), oz);
+      if constexpr (POST && WIDE) {
+        lds[slot(1, i, 0)] += f32x4{f[0], f[1], f[2], f[3]};
+        lds[slot(1, i, 1)] += f32x4{f[4], f[5], f[6], f[7]};
       }
     }
+    if constexpr (WIDE) next.load(a, row + walkers, at);  // (over the registers that are free now)
     float post_mean = 0.0f;
-    if constexpr (POST) post_mean = row_sum<WAVES>(s, posts[phase], wave, lane) / cols;
+    if constexpr (POST) {
+      post_mean = row_sum<WAVES>(s, posts[phase], wave, lane) / cols;
+      hide(c.x);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       u32x4 o;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if constexpr (POST) v[i][e] = post * (v[i][e] - element(xv[i], e) * post * post_mean);
+      for (int q = 0; q < 4; ++q) {
+        apart();
+        float x[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(v[i][2 * q], v[i][2 * q + 1]);
-      store8(dx, at(i), a.cols, o);
+        for (int k = 0; k < 2; ++k) {
+          const int e = 2 * q + k;
+          x[k] = POST ? c.post * (v[i][e] - element(c.x[i], e) * c.post * post_mean) : v[i][e];
+        }
+        o[q] = pack_bf16x2(x[0], x[1]);
+      }
+      dx.store(at(i), o);
     }
   }
   const bool alone = a.partial_rows == 1;
   float* p = a.partials + (int64_t)blockIdx.x * a.cols * (POST ? 2 : 1);
-  put_sums<WAVES>(a, dw, alone ? a.dweight : p, t, wave, lane);
-  if constexpr (POST) put_sums<WAVES>(a, dpw, alone ? a.dpost_weight : p + a.cols, t, wave, lane);
+#pragma unroll
+  for (int which = 0; which < (POST ? 2 : 1); ++which) {
+    float* to = which == 0 ? (alone ? a.dweight : p) : (alone ? a.dpost_weight : p + a.cols);
+    if constexpr (WAVES == 1) {
+      // The four waves' sums, added in order.
+      __shared__ float all[4][NV * 512];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) all[wave][at(i) + e] = which == 0 ? dw[i][e] : dpw[POST ? i : 0][e];
+      __syncthreads();
+      for (int64_t k = threadIdx.x; k < a.cols; k += 256) to[k] = ((all[0][k] + all[1][k]) + all[2][k]) + all[3][k];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          f32x4 v;
+          if constexpr (WIDE) v = lds[slot(which, i, half)];
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = which == 0 ? dw[i][4 * half + e] : dpw[POST ? i : 0][4 * half + e];
+          const int64_t k = at(i) + 4 * half;
+          if (k + 4 <= a.cols) {
+            // (16-byte stores, which need an address that is a multiple of 4.)
+            typedef float f32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+            *reinterpret_cast<f32x4_4*>(to + k) = v;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (k + e < a.cols) to[k + e] = v[e];
+          }
+        }
+    }
+  }
 }
 
 // The sum over partial rows of column c of `width` (cols, twice with a norm
@@ -369,14 +431,15 @@ block_norm_fn forward_of(bool gate, int y) {
                        : (y == kRowE4M3 ? block_norm_forward<WAVES, NV, false, kRowE4M3>
                                         : block_norm_forward<WAVES, NV, false, kRowInt8>);
 }
-template <int WAVES, int NV>
+template <int WAVES, int NV, bool WIDE>
 block_norm_fn backward_of(bool gate, bool post) {
-  if (gate) return post ? block_norm_backward<WAVES, NV, true, true> : block_norm_backward<WAVES, NV, true, false>;
-  return post ? block_norm_backward<WAVES, NV, false, true> : block_norm_backward<WAVES, NV, false, false>;
+  if (gate)
+    return post ? block_norm_backward<WAVES, NV, true, true, WIDE> : block_norm_backward<WAVES, NV, true, false, WIDE>;
+  return post ? block_norm_backward<WAVES, NV, false, true, WIDE> : block_norm_backward<WAVES, NV, false, false, WIDE>;
 }
-// (16 waves: rows of up to kBlockNormMaxCols take two vectors a lane.)
 block_norm_fn forward_pick(NormShape s, bool gate, int y) {
-  if (s.waves == 16) return s.vectors == 1 ? forward_of<16, 1>(gate, y) : forward_of<16, 2>(gate, y);
+  if (s.waves == 16) return forward_of<16, 1>(gate, y);
+  if (s.waves == 8) return forward_of<8, 4>(gate, y);
   if (s.waves == 4)
     return s.vectors == 1 ? forward_of<4, 1>(gate, y)
                           : (s.vectors == 2 ? forward_of<4, 2>(gate, y) : forward_of<4, 4>(gate, y));
@@ -384,18 +447,55 @@ block_norm_fn forward_pick(NormShape s, bool gate, int y) {
                         : (s.vectors == 2 ? forward_of<1, 2>(gate, y) : forward_of<1, 4>(gate, y));
 }
 block_norm_fn backward_pick(NormShape s, bool gate, bool post) {
-  if (s.waves == 16) return s.vectors == 1 ? backward_of<16, 1>(gate, post) : backward_of<16, 2>(gate, post);
-  if (s.waves == 4)
-    return s.vectors == 1 ? backward_of<4, 1>(gate, post)
-                          : (s.vectors == 2 ? backward_of<4, 2>(gate, post) : backward_of<4, 4>(gate, post));
-  return s.vectors == 1 ? backward_of<1, 1>(gate, post)
-                        : (s.vectors == 2 ? backward_of<1, 2>(gate, post) : backward_of<1, 4>(gate, post));
+  if (s.waves == 16) return backward_of<16, 1, false>(gate, post);
+  if (s.waves == 8) return s.vectors == 2 ? backward_of<8, 2, false>(gate, post) : backward_of<8, 4, true>(gate, post);
+  if (s.waves == 4) return s.vectors == 1 ? backward_of<4, 1, false>(gate, post) : backward_of<4, 2, false>(gate, post);
+  return s.vectors == 1 ? backward_of<1, 1, false>(gate, post) : backward_of<1, 2, false>(gate, post);
 }
+// LDS of the wide backward kernel: both weights' sums of 16384 columns.
+constexpr int kWideLds = 2 * 4 * (int)kBlockNormMaxCols;
 
 }  // namespace
 
+// Forward, the norm's shapes, but rows of more than 8192 columns are shared by
+// eight waves.
+NormShape block_norm_forward_shape(int64_t rows, int64_t cols) {
+  if (cols > 8192) return {8, 4};
+  return norm_shape(rows, cols);
+}
+
+// Backward a lane holds up to two vectors of a row (of five matrices, their
+// sums and the next row's), or four with the sums in LDS.  Few rows, whose
+// latency counts: one vector.
+NormShape block_norm_backward_shape(int64_t rows, int64_t cols) {
+  if (cols > 8192) return {8, 4};
+  if (rows <= 256) return cols <= 512 ? NormShape{1, 1} : (cols <= 2048 ? NormShape{4, 1} : NormShape{16, 1});
+  if (cols <= 1024) return {1, cols <= 512 ? 1 : 2};
+  if (cols <= 4096) return {4, cols <= 2048 ? 1 : 2};
+  return {8, 2};
+}
+
+// A second kernel costs about as much as three rows one after another.  As many
+// workgroups as the chip holds at once.
+int64_t block_norm_partial_rows(int64_t rows, int64_t cols, int cu_count) {
+  const int waves = block_norm_backward_shape(rows, cols).waves, at_once = rows_of(waves);
+  if (rows <= 3 * at_once) return rows > 0 ? 1 : 0;
+  const int64_t groups = (rows + at_once - 1) / at_once, most = (int64_t)cu_count * (waves <= 4 ? 2 : 1);
+  return groups < most ? groups : most;
+}
+
+hipError_t prepare_block_norm() {
+  for (bool gate : {false, true})
+    for (bool post : {false, true}) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(backward_of<8, 4, true>(gate, post)),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, kWideLds);
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
+}
+
 hipError_t launch_block_norm_forward(const BlockNormArgs& a, int y_type, hipStream_t stream) {
-  const NormShape s = norm_shape(a.rows, a.cols);
+  const NormShape s = block_norm_forward_shape(a.rows, a.cols);
   const block_norm_fn f = forward_pick(s, a.z != nullptr, y_type);
   int64_t grid = (a.rows + rows_of(s.waves) - 1) / rows_of(s.waves);
   if (grid > (1 << 20)) grid = 1 << 20;  // a launch holds fewer than 2^32 threads
@@ -404,11 +504,12 @@ hipError_t launch_block_norm_forward(const BlockNormArgs& a, int y_type, hipStre
 }
 
 hipError_t launch_block_norm_backward(const BlockNormArgs& a, hipStream_t stream) {
-  const NormShape s = norm_shape(a.rows, a.cols);
+  const NormShape s = block_norm_backward_shape(a.rows, a.cols);
   const bool post = a.dpost_weight != nullptr;
   if (a.partial_rows > 0) {
     const block_norm_fn f = backward_pick(s, a.dz != nullptr, post);
-    hipLaunchKernelGGL(f, dim3((uint32_t)a.partial_rows), dim3(threads_of(s.waves)), 0, stream, a);
+    hipLaunchKernelGGL(f, dim3((uint32_t)a.partial_rows), dim3(threads_of(s.waves)), s.vectors == 4 ? kWideLds : 0, stream,
+                       a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.partial_rows == 1) return e;
   }

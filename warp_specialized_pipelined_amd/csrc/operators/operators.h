@@ -85,7 +85,12 @@ struct BlockNormArgs {
 };
 
 // Widest row the kernels hold in registers.
-constexpr int64_t kBlockNormMaxCols = 16 * 64 * 2 * 8;
+constexpr int64_t kBlockNormMaxCols = 8 * 64 * 4 * 8;
+NormShape block_norm_forward_shape(int64_t rows, int64_t cols);
+NormShape block_norm_backward_shape(int64_t rows, int64_t cols);
+// Rows of partial column sums the backward pass leaves in its workspace.
+int64_t block_norm_partial_rows(int64_t rows, int64_t cols, int cu_count);
+hipError_t prepare_block_norm();
 
 // y_type: 0 bf16, 1 e4m3, 2 int8.
 hipError_t launch_block_norm_forward(const BlockNormArgs& a, int y_type, hipStream_t stream);

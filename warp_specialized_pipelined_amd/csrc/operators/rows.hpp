@@ -57,6 +57,52 @@ __device__ __forceinline__ void store8_bytes(unsigned char* row, int64_t c, int6
     for (int e = 0; e < (int)(cols - c); ++e) row[c + e] = (unsigned char)(v[e >> 2] >> (8 * (e & 3)));
   }
 }
+// A row through a buffer resource over its columns: what a lane has past them
+// reads as zeros and is not written, without branches (range checks work on
+// dwords; the element or bytes in a last, partial one are seen to apart).
+// Wave-uniform.
+struct RowView {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int cols;
+  // bf16 to be read: the range ends with the last dword.
+  static __device__ __forceinline__ RowView in(const void* m, int64_t elements, int64_t cols) {
+    return {make_rsrc(static_cast<const unsigned short*>(m) + elements, (uint32_t)((cols * 2 + 3) & ~(int64_t)3)), (int)cols};
+  }
+  // To be written: the range ends with the last element (of ES bytes).
+  template <int ES>
+  static __device__ __forceinline__ RowView out(void* m, int64_t elements, int64_t cols) {
+    return {make_rsrc(static_cast<unsigned char*>(m) + elements * ES, (uint32_t)(cols * ES)), (int)cols};
+  }
+  // Eight bf16 at column c.
+  __device__ __forceinline__ u32x4 load(int c) const {
+    u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, 2 * c, 0, 0));
+    if (cols & 1) {
+      const int last = (cols - c) >> 1;  // the dword that holds the last column
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v[w] = w == last ? v[w] & 0xFFFFu : v[w];
+    }
+    return v;
+  }
+  __device__ __forceinline__ void store(int c, u32x4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, 2 * c, 0, 0);
+    if (cols & 1) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (w == (cols - c) >> 1) __builtin_amdgcn_raw_buffer_store_b16((unsigned short)v[w], rsrc, 2 * (c + 2 * w), 0, 0);
+    }
+  }
+  // Eight bytes at column c.
+  __device__ __forceinline__ void store_bytes(int c, u32x2 v) const {
+    __builtin_amdgcn_raw_buffer_store_b64(v, rsrc, c, 0, 0);
+    if (cols & 3) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (w == (cols - c) >> 2)
+          for (int b = 0; b < (cols & 3); ++b)
+            __builtin_amdgcn_raw_buffer_store_b8((unsigned char)(v[w] >> (8 * b)), rsrc, c + 4 * w + b, 0, 0);
+    }
+  }
+};
 // The larger of each half's unsigned 16 bits.
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
