@@ -32,13 +32,21 @@ enum RowType { kRowBf16, kRowE4M3, kRowInt8 };
 __device__ __forceinline__ float element(const u32x4& v, int e) { return e & 1 ? hi(v[e >> 1]) : lo(v[e >> 1]); }
 
 // s = 1 / (1 + exp(-z)) and its derivative s (1 - s), both from exp(-|z|): no
-// overflow, and nothing lost where s is next to 1.
+// overflow, and nothing lost where s is next to 1.  What the product with log2 e
+// rounds off is put back (or exp would be off by |z| 2^-24), and the reciprocal
+// is refined: a code of y changes where its value crosses a border of two, which
+// it does as often as h is off.
 struct Gate {
   float s, ds;
   __device__ __forceinline__ explicit Gate(float z) {
-    const float e = __builtin_amdgcn_exp2f(-fabsf(z) * 1.4426950408889634f), r = __builtin_amdgcn_rcpf(1.0f + e);
+    constexpr float kLog2e = 1.44269502f, kRest = 1.92596302e-8f, kLn2 = 0.693147182f;  // log2 e in two parts
+    const float m = fminf(fabsf(z), 128.0f);  // (exp is 0 in fp32 from 104 on)
+    const float t = -m * kLog2e, rest = -m * kRest - fmaf(m, kLog2e, t);
+    const float x = __builtin_amdgcn_exp2f(t), e = fmaf(x, rest * kLn2, x);
+    const float d = 1.0f + e, q = __builtin_amdgcn_rcpf(d), r = fmaf(q, fmaf(-d, q, 1.0f), q);
     s = z < 0.0f ? e * r : r;
     ds = e * r * r;
+    if (z != z) s = ds = z;
   }
 };
 
