@@ -192,9 +192,10 @@ __global__ __launch_bounds__(64) void checkpoint_unpack(CheckpointArgs a, int64_
 // TM x TN tiles of dw (kepttile.hpp), a workgroup for each of a tile's `splits`
 // ranges of the tokens.  With one it stores the result; with more each stores
 // its fp32 sums in register order, and kept_join adds them up.
-template <int TM, int TN, int SLOTS, int WAVES>
-__global__ __launch_bounds__(256, WAVES) void kept_gradient(CheckpointArgs a) {
-  constexpr int BM = TM / 64, BN = TN / 64;
+template <int TM, int TN, int SLOTS, int WM, int WN, int PER_SIMD>
+__global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void kept_gradient(CheckpointArgs a) {
+  typedef KeptGeom<TM, TN, SLOTS, WM, WN> T;
+  constexpr int BM = T::kBM, BN = T::kBN;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int tiles_m = (int)((a.out_cols + TM - 1) / TM), tiles_n = (int)((a.cols + TN - 1) / TN);
   const int slot = persistent_slot(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
@@ -203,13 +204,13 @@ __global__ __launch_bounds__(256, WAVES) void kept_gradient(CheckpointArgs a) {
   const int stages = (int)((a.tokens + kKeptTokens - 1) / kKeptTokens);
   const int k0 = (int)((int64_t)stages * split / a.splits), k1 = (int)((int64_t)stages * (split + 1) / a.splits);
   MidAccum<BM, BN> acc;
-  kept_loop<TM, TN, SLOTS>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0, k1 - k0);
+  kept_loop<TM, TN, SLOTS, WM, WN>(acc, a, (int64_t)t.tm * TM, (int64_t)t.tn * TN, wave, lane, k0, k1 - k0);
   if (a.splits > 1) {
-    mid_put(a.partials, slot, acc, wave, lane);
+    mid_put(a.partials, slot * (T::kWaves / 4) + wave / 4, acc, wave % 4, lane);
     return;
   }
-  const int64_t m0 = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM;
-  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN;
+  const int64_t m0 = (int64_t)t.tm * TM + wave / WN * 32 * BM;
+  const int64_t n0 = (int64_t)t.tn * TN + wave % WN * 32 * BN;
   if (!a.fp32) {
     mid_store<BM, BN>(
         a.dw, a.dw_rs, a.out_cols, a.cols, m0, n0, wave, lane,
@@ -227,20 +228,21 @@ __global__ __launch_bounds__(256, WAVES) void kept_gradient(CheckpointArgs a) {
 
 // The ranges' sums of one 32 x 32 block, added in order and stored: a wave a
 // block.
-template <int TM, int TN>
+template <int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(64) void kept_join(CheckpointArgs a) {
-  constexpr int BM = TM / 64, BN = TN / 64;
+  constexpr int BM = TM / (32 * WM), BN = TN / (32 * WN);
   const int lane = threadIdx.x;
   const int tiles_m = (int)((a.out_cols + TM - 1) / TM), tiles_n = (int)((a.cols + TN - 1) / TN);
-  const int part = blockIdx.x % (4 * BM * BN), tile = blockIdx.x / (4 * BM * BN);
+  const int part = blockIdx.x % (WM * WN * BM * BN), tile = blockIdx.x / (WM * WN * BM * BN);
   const int wave = part / (BM * BN), block = part % (BM * BN);
   const MidTile t = mid_tile(tile, tiles_m, tiles_n);
-  const int64_t m = (int64_t)t.tm * TM + (wave >> 1) * 32 * BM + 32 * (block / BN) + (lane & 31);
-  const int64_t n0 = (int64_t)t.tn * TN + (wave & 1) * 32 * BN + 32 * (block % BN);
+  const int64_t m = (int64_t)t.tm * TM + wave / WN * 32 * BM + 32 * (block / BN) + (lane & 31);
+  const int64_t n0 = (int64_t)t.tn * TN + wave % WN * 32 * BN + 32 * (block % BN);
   if (m - (lane & 31) >= a.out_cols || n0 >= a.cols) return;
   MidAccum<1, 1> acc = {};
 #pragma unroll 4
-  for (int i = 0; i < a.splits; ++i) mid_add<BM, BN>(a.partials, i * tiles_m * tiles_n + tile, acc, wave, block, lane);
+  for (int i = 0; i < a.splits; ++i) 
+    mid_add<BM, BN>(a.partials, (int64_t)(i * tiles_m * tiles_n + tile) * (WM * WN / 4) + wave / 4, acc, wave % 4, block, lane);
   if (m >= a.out_cols) return;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -259,7 +261,7 @@ __global__ __launch_bounds__(64) void kept_join(CheckpointArgs a) {
 }
 
 struct KeptVariant {
-  int tm, tn, slots, lds;
+  int tm, tn, slots, threads, lds;
   void (*kernel)(CheckpointArgs);
   void (*join)(CheckpointArgs);
   // What its tiles cost (choose_checkpoint), in microseconds: a stage with one
@@ -267,16 +269,16 @@ struct KeptVariant {
   int per_cu;
   double stage1, stage2, tile;
 };
-template <int TM, int TN, int SLOTS, int WAVES>
+template <int TM, int TN, int SLOTS, int WM, int WN, int PER_SIMD>
 constexpr KeptVariant kept_variant(int per_cu, double stage1, double stage2, double tile) {
-  return {TM, TN, SLOTS, (int)KeptGeom<TM, TN, SLOTS>::kLds, kept_gradient<TM, TN, SLOTS, WAVES>, kept_join<TM, TN>,
-          per_cu, stage1, stage2, tile};
+  return {TM, TN, SLOTS, 64 * WM * WN, (int)KeptGeom<TM, TN, SLOTS, WM, WN>::kLds,
+          kept_gradient<TM, TN, SLOTS, WM, WN, PER_SIMD>, kept_join<TM, TN, WM, WN>, per_cu, stage1, stage2, tile};
 }
 const KeptVariant kVariants[] = {
-    kept_variant<256, 256, 3, 1>(1, 1.23, 1.13, 7.3),
-    kept_variant<192, 256, 3, 1>(1, 0.89, 0.83, 6.5),
-    kept_variant<128, 128, 3, 2>(2, 0.50, 0.70, 2.1),
-    kept_variant<64, 64, 4, 3>(3, 0.27, 0.52, 1.3),
+    kept_variant<256, 256, 3, 2, 4, 2>(1, 1.15, 1.10, 5.5),
+    kept_variant<192, 256, 3, 2, 4, 2>(1, 0.83, 0.80, 5.0),
+    kept_variant<128, 128, 3, 2, 2, 2>(2, 0.50, 0.70, 2.1),
+    kept_variant<64, 64, 4, 2, 2, 3>(3, 0.27, 0.52, 1.3),
 };
 int64_t tiles_of(const KeptVariant& v, int64_t out_cols, int64_t cols) {
   return ((out_cols + v.tm - 1) / v.tm) * ((cols + v.tn - 1) / v.tn);
@@ -345,7 +347,7 @@ hipError_t prepare_checkpoint() {
 hipError_t launch_checkpoint_gradient(const CheckpointArgs& a, int variant, hipStream_t stream) {
   const KeptVariant& v = kVariants[variant];
   const int64_t tiles = tiles_of(v, a.out_cols, a.cols);
-  hipLaunchKernelGGL(v.kernel, dim3((uint32_t)(tiles * a.splits)), dim3(256), v.lds, stream, a);
+  hipLaunchKernelGGL(v.kernel, dim3((uint32_t)(tiles * a.splits)), dim3(v.threads), v.lds, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL(v.join, dim3((uint32_t)(tiles * (v.tm / 32) * (v.tn / 32))), dim3(64), 0, stream, a);

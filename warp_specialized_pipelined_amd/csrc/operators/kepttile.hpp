@@ -35,14 +35,16 @@ namespace migemm {
 
 constexpr int kKeptTokens = 64;  // a stage
 
-template <int TM, int TN, int SLOTS>
+template <int TM, int TN, int SLOTS, int WM, int WN>
 struct KeptGeom {
-  static constexpr int kBM = TM / 64, kBN = TN / 64;  // a wave's 32 x 32 blocks
-  static constexpr int kLoadsA = TM / 32, kLoadsB = TN / 64, kLoads = kLoadsA + kLoadsB + 1;  // of a wave and stage
-  static constexpr uint32_t kCodes = TM * 128, kPowers = kCodes + TN * kKeptTokens, kSlot = kPowers + 4 * 256;
+  static constexpr int kWaves = WM * WN;
+  static constexpr int kBM = TM / (32 * WM), kBN = TN / (32 * WN);  // a wave's 32 x 32 blocks
+  static constexpr int kLoadsA = TM / (8 * kWaves), kLoadsB = TN / (16 * kWaves);
+  static constexpr int kLoads = kLoadsA + kLoadsB + 1;  // of a wave and stage
+  static constexpr uint32_t kCodes = TM * 128, kPowers = kCodes + TN * kKeptTokens, kSlot = kPowers + kWaves * 256;
   static constexpr uint32_t kRing = SLOTS * kSlot;
   // Epilogue staging, of each wave: bf16, all its rows; fp32, 32 at a time.
-  static constexpr uint32_t kStaging16 = 4 * 32 * kBM * (64 * kBN + 16), kStaging32 = 4 * 32 * (128 * kBN + 16);
+  static constexpr uint32_t kStaging16 = kWaves * 32 * kBM * (64 * kBN + 16), kStaging32 = kWaves * 32 * (128 * kBN + 16);
   static constexpr uint32_t kStaging = kStaging16 > kStaging32 ? kStaging16 : kStaging32;
   static constexpr uint32_t kLds = kRing > kStaging ? kRing : kStaging;
   static_assert(kLds <= kLdsLimit && (SLOTS - 2) * kLoads < 64, "the ring fits LDS, its loads vmcnt");
@@ -120,7 +122,7 @@ struct KeptDyLoader {
 // The codes' and powers' loads of a stage.  Groups of tokens past the kept ones
 // read as zero; columns past the last read other codes, or zeros, for columns
 // of dw that are not stored.
-template <int TN, int BN, int NL>
+template <int TN, int BN, int WN, int NL>
 struct KeptLoader {
   uint64_t codes_at, powers_at;  // the next stage's
   int64_t codes_left, powers_left, ld;
@@ -130,7 +132,7 @@ struct KeptLoader {
     ld = a.ld;
     codes_at = reinterpret_cast<uint64_t>(a.codes) + ((int64_t)stage * 4 * ld + k0) * 16;
     codes_left = groups * 32 * ld - ((int64_t)stage * 4 * ld + k0) * 16;
-    const int64_t col = k0 + (wave & 1) * 32 * BN;
+    const int64_t col = k0 + wave % WN * 32 * BN;
     powers_at = reinterpret_cast<uint64_t>(a.scales) + (int64_t)stage * 2 * ld + col;
     powers_left = groups * ld - (int64_t)stage * 2 * ld - col;
 #pragma unroll
@@ -156,20 +158,18 @@ struct KeptLoader {
 };
 
 // Stages [k0, k0 + KT) of the tile at (m0, n0).  On return every wave is done with the ring.
-// WAVE: the wave, as a constant: each issues its loads at its own products.
-template <int TM, int TN, int SLOTS, int WAVE>
-__device__ __forceinline__ void kept_loop_of(MidAccum<TM / 64, TN / 64>& acc, const CheckpointArgs& a, int64_t m0,
-                                             int64_t n0, int lane, int k0, int KT) {
-  constexpr int wave = WAVE;
-  typedef KeptGeom<TM, TN, SLOTS> T;
+template <int TM, int TN, int SLOTS, int WM, int WN, class Acc>
+__device__ __forceinline__ void kept_loop(Acc& acc, const CheckpointArgs& a, int64_t m0, int64_t n0, int wave,
+                                          int lane, int k0, int KT) {
+  typedef KeptGeom<TM, TN, SLOTS, WM, WN> T;
   constexpr int BM = T::kBM, BN = T::kBN, NLA = T::kLoadsA, NLB = T::kLoadsB, P = BM * BN;
   KeptDyLoader<NLA> la;
-  KeptLoader<TN, BN, NLB> lb;
+  KeptLoader<TN, BN, WN, NLB> lb;
   la.init(a, m0, k0, wave, lane);
   lb.init(a, n0, k0, wave, lane);
   KeptReader<BM> ra;
-  ra.init((wave >> 1) * 32 * BM, lane);
-  const uint32_t code_at = T::kCodes + ((lane >> 5) * TN + (wave & 1) * 32 * BN + (lane & 31)) * 16;
+  ra.init(wave / WN * 32 * BM, lane);
+  const uint32_t code_at = T::kCodes + ((lane >> 5) * TN + wave % WN * 32 * BN + (lane & 31)) * 16;
   const uint32_t power_at = T::kPowers + wave * 256 + (lane & 31);
 #pragma unroll
   for (int i = 0; i < BM; ++i)
@@ -247,10 +247,7 @@ __device__ __forceinline__ void kept_loop_of(MidAccum<TM / 64, TN / 64>& acc, co
     const auto sb = lb.next();
     auto loads = [&](auto first, auto mc) {
       constexpr int m = decltype(first)::value * P + decltype(mc)::value;
-      // Load j stands behind product (j + wave / 4) 4 P / kLoads of the stage's 4 P.
-      static_for<0, T::kLoads>([&](auto jc) {
-        if constexpr ((4 * decltype(jc)::value + WAVE) * P / T::kLoads == m) load(sa, sb, jc, cur);
-      });
+      static_for<m * T::kLoads / (4 * P), (m + 1) * T::kLoads / (4 * P)>([&](auto jc) { load(sa, sb, jc, cur); });
     };
     step(std::integral_constant<int, 3>{}, nxt, [&](auto mc) { loads(std::integral_constant<int, 0>{}, mc); });
     static_for<0, 3>([&](auto kc) {
@@ -267,15 +264,6 @@ __device__ __forceinline__ void kept_loop_of(MidAccum<TM / 64, TN / 64>& acc, co
   wait_vmcnt<0>();
   wait_lgkmcnt<0>();
   barrier();
-}
-
-template <int TM, int TN, int SLOTS>
-__device__ __forceinline__ void kept_loop(MidAccum<TM / 64, TN / 64>& acc, const CheckpointArgs& a, int64_t m0,
-                                          int64_t n0, int wave, int lane, int k0, int KT) {
-  if (wave == 0) kept_loop_of<TM, TN, SLOTS, 0>(acc, a, m0, n0, lane, k0, KT);
-  else if (wave == 1) kept_loop_of<TM, TN, SLOTS, 1>(acc, a, m0, n0, lane, k0, KT);
-  else if (wave == 2) kept_loop_of<TM, TN, SLOTS, 2>(acc, a, m0, n0, lane, k0, KT);
-  else kept_loop_of<TM, TN, SLOTS, 3>(acc, a, m0, n0, lane, k0, KT);
 }
 
 // The wave's part of the tile in fp32, 32 rows at a time staged through LDS
