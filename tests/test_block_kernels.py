@@ -10,20 +10,18 @@ from tests.test_int8 import Int8
 
 # (rows, columns, stages of K in LDS, K split) of a kernel, and sizes that reach it.
 INT8 = [
-    ((256, 256, 2, False), [(2900, 4100, 2057), (4601, 2909, 655)]),
-    ((192, 256, 2, False), [(790, 10137, 537), (1643, 5325, 519)]),
-    ((16, 16, 0, False), [(17, 33, 300), (1, 17, 18)]),
-    ((16, 32, 0, False), [(1, 4839, 16), (300, 500, 2001)]),
-    ((32, 32, 0, False), [(127, 3001, 385), (5516, 17, 16)]),
-    ((64, 32, 0, False), [(33, 6497, 310), (4193, 68, 16)]),
-    ((64, 64, 4, False), [(1001, 1003, 1001), (1, 15679, 1378)]),
-    ((64, 64, 4, True), [(190, 321, 16001), (1, 17, 13938)]),
-    ((64, 128, 3, False), [(513, 4097, 1001), (479, 2921, 17)]),
-    ((64, 128, 3, True), [(142, 752, 13655), (1, 1351, 16240)]),
-    ((128, 128, 4, False), [(424, 6578, 7971), (222, 8439, 1218)]),
-    ((128, 128, 4, True), [(68, 2901, 11477), (1450, 213, 10798)]),
+    ((256, 256, 2, False), [(2900, 4100, 2057), (884, 15509, 1752)]),
+    ((192, 256, 2, False), [(1426, 6120, 397), (1643, 5325, 519)]),
+    ((16, 16, 0, False), [(17, 33, 4001), (1, 16, 3631)]),
+    ((16, 32, 0, False), [(36, 1454, 4187), (33, 1806, 4010)]),
+    ((32, 32, 0, False), [(127, 3001, 385), (1, 17, 18), (5516, 17, 16)]),
+    ((64, 32, 0, False), [(40, 9675, 18), (5485, 79, 19)]),
+    ((64, 64, 4, False), [(1001, 1003, 1001), (9, 16723, 71)]),
+    ((64, 64, 4, True), [(2205, 18, 13802), (21, 2310, 13919)]),
+    ((64, 128, 3, False), [(941, 3813, 227), (149, 12849, 16)]),
+    ((64, 128, 3, True), [(34, 2802, 15899), (68, 1712, 13638)]),
     ((128, 128, 2, False), [(2773, 2191, 552), (8362, 403, 19)]),
-    ((128, 128, 2, True), [(1200, 2000, 9001), (5783, 142, 9784)]),
+    ((128, 128, 2, True), [(5933, 42, 15399), (1200, 2000, 9001)]),
 ]
 
 

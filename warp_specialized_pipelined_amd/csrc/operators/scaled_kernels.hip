@@ -23,7 +23,7 @@ namespace {
 // two slots); two slots, two workgroups a unit, each loading while the other
 // multiplies, where there are more (1600 x 4000 x 16000: 125 us, 149 with 192
 // rows a tile, 165 with 64 x 128; 2773 x 2191 x 552: 15.0, 25.6 and 18.4).
-enum { kExactRows = kChosen, kExactMid };
+enum { kMidLast = 9, kExactRows, kExactMid };
 const Variant kVariants[] = {
     tile_variant<kMulNative, 4>(1.1, 7.0),
     tile_variant<kMulNative, 3>(0.95, 6.0),
@@ -38,6 +38,7 @@ const Variant kVariants[] = {
     rows_variant<kExactE4M3, 1, 4, 2, 1>(2),
     mid_variant<kMulExact, 64, 64, 2>(2, 0, 0, 0),
 };
+const CostModel kCost = {kMidLast, 5.5e6, 0.26, 0.6, false, 4.0, 5.2e6};
 
 }  // namespace
 
@@ -55,7 +56,7 @@ ScaledChoice choose_scaled(int64_t M, int64_t N, int64_t K, int cu_count) {
   // and 9.4; 2000 x 4096 x 1024: 31.5 and 13.5), where longer sums average the
   // loss out.
   if (K <= 256) return {M <= 16 ? kExactRows : kExactMid, 1, kTileM, 0};
-  return cheapest_variant(kVariants, M, N, K, cu_count);
+  return cheapest_variant(kCost, kVariants, M, N, K, cu_count);
 }
 
 ScaledKernel scaled_kernel(int variant) {

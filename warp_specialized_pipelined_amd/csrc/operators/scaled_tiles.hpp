@@ -199,8 +199,9 @@ struct Variant {
   void (*kernel)(ScaledArgs);
   void (*join)(ScaledArgs);
   int per_cu;  // tiles a compute unit takes at once, for the cost
-  // What its tiles cost (cheapest_variant), in microseconds: a K stage of 128
-  // with one tile a compute unit and with two, and a tile besides.
+  // What its tiles cost (cost_of), in microseconds: a K stage of 128 with one
+  // tile a compute unit and with two, and a tile besides; of a rows variant the
+  // bytes that a compute unit takes in in one, and the launch besides.
   double stage1, stage2, tile;
 };
 template <MidMul MUL, int BM>
@@ -208,50 +209,65 @@ constexpr Variant tile_variant(double stage, double tile) {
   return {64 * BM, kTileN, kThreads, kPlainLdsBytes, scaled_tile<MUL, BM>, nullptr, 1, stage, stage, tile};
 }
 template <int ES, int MB, int NB, int W, int U>
-constexpr Variant rows_variant(int per_cu) {
-  return {16 * MB, 16 * NB, 64 * W, 0, scaled_rows<ES, MB, NB, W, U>, nullptr, per_cu, 0, 0, 0};
+constexpr Variant rows_variant(int per_cu, double bytes = 52e3, double launch = 0) {
+  return {16 * MB, 16 * NB, 64 * W, 0, scaled_rows<ES, MB, NB, W, U>, nullptr, per_cu, bytes, bytes, launch};
 }
 template <MidMul MUL, int TM, int TN, int SLOTS>
 constexpr Variant mid_variant(int per_cu, double stage1, double stage2, double tile) {
   return {TM, TN, 256, (int)MidGeom<TM, TN, SLOTS>::kLds, scaled_mid<MUL, TM, TN, SLOTS>,
           MUL == kMulExact ? nullptr : scaled_join<MUL == kMulInt8, TM, TN>, per_cu, stage1, stage2, tile};
 }
-// A table of variants starts with these; what follows is chosen by other rules.
-enum { kTile256, kTile192, kRowsFirst, kRowsLast = 5, kMidFirst, kMidLast = 9, kChosen };
+// A table of variants starts with these, then has its mid variants.
+enum { kTile256, kTile192, kRowsFirst, kRowsLast = 5, kMidFirst };
 
 inline int64_t tiles_of(const Variant& v, int64_t M, int64_t N) {
   return ((M + v.tm - 1) / v.tm) * ((N + v.tn - 1) / v.tn);
 }
-// Microseconds that v's kernel takes, after what the launch takes.
-inline double cost_of(const Variant& v, bool rows, int64_t M, int64_t N, int64_t K, int splits, int cu_count) {
+// What the costs of a table's variants share.
+struct CostModel {
+  int last;          // the last variant that is chosen by its cost
+  double memory;     // bytes a microsecond
+  // Rows variants: the part of the lesser of memory's and the compute unit's
+  // time that the greater does not hide; a round of two tiles a unit, besides.
+  // (existing: of a tile's rows only those that the matrix has are read.)
+  double overlap, round;
+  bool existing;
+  double join, put;  // a split's: microseconds, and bytes of the sums a microsecond
+};
+// Microseconds that a kernel takes, after what the launch takes.
+inline double cost_of(const CostModel& m, const Variant* variants, int variant, int64_t M, int64_t N, int64_t K,
+                      int splits, int cu_count) {
+  const Variant& v = variants[variant];
   const double tiles = (double)tiles_of(v, M, N), cus = cu_count;
-  const double memory = ((double)M * K + (double)N * K + 2.0 * M * N) / 5.5e6;
-  if (rows) {
+  const double memory = ((double)M * K + (double)N * K + 2.0 * M * N) / m.memory;
+  if (variant >= kRowsFirst && variant <= kRowsLast) {
     // What a compute unit takes in, and the memory; they overlap in part.
     const double rounds = tiles <= cus ? 1.0 : (v.per_cu == 1 ? ceil(tiles / cus) : tiles / cus);
-    const double cu = rounds * (v.tm + v.tn) * K / 52e3;
-    return (cu > memory ? cu + 0.26 * memory : memory + 0.26 * cu) + 0.6 * ceil(tiles / (2 * cus));
+    const double rows = m.existing && M < v.tm ? M : v.tm;
+    const double cu = rounds * (rows + v.tn) * K / v.stage1;
+    return (cu > memory ? cu + m.overlap * memory : memory + m.overlap * cu) + m.round * ceil(tiles / (2 * cus)) +
+           v.tile;
   }
   const double stages = ceil(ceil(K / 128.0) / splits), items = tiles * splits;
   const double at_once = v.per_cu * cus, full = floor(items / at_once), rest = items - full * at_once;
   double t = full * (stages * v.stage2 + v.tile);
   if (rest > 0) t += stages * (rest <= cus ? v.stage1 : v.stage2) + v.tile;
   t = t > memory ? t : memory;
-  if (splits > 1) t += 4.0 + 2 * items * v.tm * v.tn * 4 / 5.2e6;  // scaled_join, and its sums to memory and back
+  if (splits > 1) t += m.join + 2 * items * v.tm * v.tn * 4 / m.put;  // scaled_join, and its sums to memory and back
   return t;
 }
 
 // The variant that costs least.
-inline ScaledChoice cheapest_variant(const Variant* variants, int64_t M, int64_t N, int64_t K, int cu_count) {
+inline ScaledChoice cheapest_variant(const CostModel& model, const Variant* variants, int64_t M, int64_t N, int64_t K,
+                                     int cu_count) {
   ScaledChoice best = {kTile256, 1, kTileM, 0};
   double least = 1e300;
   // (Past 2^30 results only the large tiles, whose count stays within 31 bits.)
-  const int last = (double)M * N > 1e9 ? kTile192 : kMidLast;
+  const int last = (double)M * N > 1e9 ? kTile192 : model.last;
   for (int i = kTile256; i <= last; ++i)
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (splits > 1 && (i < kMidFirst || K < 128 * 3 * splits)) break;
-      const double cost =
-          cost_of(variants[i], i >= kRowsFirst && i <= kRowsLast, M, N, K, splits, cu_count);
+      const double cost = cost_of(model, variants, i, M, N, K, splits, cu_count);
       if (cost >= least) continue;
       least = cost;
       best = {i, splits, kTileM, 0};
