@@ -718,7 +718,8 @@ int gemm_block_norm_run_backward(const migemm_block_norm_plan* plan, const void*
  * dy is tokens x out_cols bf16; the products are exact and the sums fp32; dw is
  * out_cols x cols, bf16 (rounded once), or fp32, to which with accumulate the
  * sum is added.  tokens may be 0 (the gradient is then 0, or unchanged).
- * tokens below 2^31 - 64; 256 rows of dy and dw span less than 2^31 bytes. */
+ * tokens below 2^31 - 64; 256 rows of dy and dw span less than 2^31 bytes,
+ * and dw has fewer than 2^38 elements (else UNSUPPORTED). */
 typedef struct migemm_checkpoint_desc {
   int64_t tokens, cols;
   int64_t x_rs;               /* bf16 */

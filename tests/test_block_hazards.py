@@ -11,7 +11,7 @@ from tests.test_asm_hazards import LDS_LOAD, check_load
 from tests.test_operator_hazards import _innermost_loops
 from warp_specialized_pipelined_amd import build as _build
 
-KERNELS = {"int8_kernels": ("scaled_", 6), "checkpoint_kernels": ("kept_gradient", 4)}
+KERNELS = {"int8_kernels": ("scaled_", 5), "checkpoint_kernels": ("kept_gradient", 4)}
 
 
 @pytest.fixture(scope="module", params=sorted(KERNELS))

@@ -39,6 +39,8 @@ def desc(tokens=40, cols=100, x_rs=104, out_cols=30, dy_rs=32, dw_rs=104, dw_typ
     (dict(dy_rs=1 << 22), UNS), (dict(dw_rs=1 << 22), UNS), (dict(dw_rs=1 << 21, dw_type=FP32), UNS),
     (dict(tokens=(1 << 31) - 64), UNS), (dict(tokens=1 << 62), UNS), (dict(x_rs=1 << 61), UNS),
     (dict(cols=1 << 24, x_rs=1 << 24, dw_rs=1 << 24), UNS),
+    (dict(cols=1 << 20, x_rs=1 << 20, dw_rs=1 << 20, out_cols=1 << 18, dy_rs=1 << 18), UNS),
+    (dict(cols=1 << 20, x_rs=1 << 20, dw_rs=1 << 20, out_cols=(1 << 18) - 8, dy_rs=1 << 18), OK),
 ])
 def test_description_status(over, status):
     assert migemm.gemm_checkpoint_desc_validate(desc(**over)) == status

@@ -118,10 +118,11 @@ int validate_checkpoint(const migemm_checkpoint_desc* d) {
   if (st == MIGEMM_OK && grad) st = check_matrix(d->out_cols, d->cols, d->dw_rs, d->dw_type == MIGEMM_FP32 ? 4 : 2);
   if (st != MIGEMM_OK) return st;
   // 64 tokens of dy and of the codes, and 256 rows of dw, are reached with
-  // 32-bit offsets; tokens are counted in 32 bits.
+  // 32-bit offsets; tokens are counted in 32 bits, and a launch of a workgroup
+  // of 512 for each 256 x 256 tile holds fewer than 2^32 threads.
   if (!band_fits(d->cols, 1) || d->tokens >= ((int64_t)1 << 31) - 64) return MIGEMM_ERR_UNSUPPORTED;
   if (grad && (!band_fits(d->dy_rs, 2) || !band_fits(d->dw_rs, d->dw_type == MIGEMM_FP32 ? 4 : 2) ||
-               !tiles_fit(d->out_cols, d->cols)))
+               d->out_cols >= ((int64_t)1 << 38) / d->cols))
     return MIGEMM_ERR_UNSUPPORTED;
   return MIGEMM_OK;
 }

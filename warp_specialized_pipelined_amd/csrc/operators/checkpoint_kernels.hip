@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64) void kept_join(CheckpointArgs a) {
   if (m - (lane & 31) >= a.out_cols || n0 >= a.cols) return;
   MidAccum<1, 1> acc = {};
 #pragma unroll 4
-  for (int i = 0; i < a.splits; ++i) 
+  for (int i = 0; i < a.splits; ++i)
     mid_add<BM, BN>(a.partials, (int64_t)(i * tiles_m * tiles_n + tile) * (WM * WN / 4) + wave / 4, acc, wave % 4, block, lane);
   if (m >= a.out_cols) return;
 #pragma unroll
@@ -313,9 +313,9 @@ CheckpointChoice choose_checkpoint(int64_t tokens, int64_t cols, int64_t out_col
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       const KeptVariant& v = kVariants[i];
       const double tiles = (double)tiles_of(v, out_cols, cols), items = tiles * splits;
-      // (A launch holds fewer than 2^32 threads.)
       if (splits > 1 && (all < 3 * splits || items * v.tm * v.tn * 4 > (512 << 20))) break;
-      if (items > (1 << 23) && i > 0) break;
+      // (A launch holds fewer than 2^32 threads; the largest tiles always fit.)
+      if (items * v.threads > 4e9 && i > 0) break;
       const double stages = ceil(all / splits), at_once = (double)v.per_cu * cu_count;
       const double full = floor(items / at_once), rest = items - full * at_once;
       double t = full * (stages * v.stage2 + v.tile);
