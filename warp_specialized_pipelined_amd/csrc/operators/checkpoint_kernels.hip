@@ -11,6 +11,11 @@
 //
 //   dw[n][k] = sum over tokens of dy[t][n] code[t][k] 2^(e[t / 32][k] - 127)
 // on the bf16 instructions: the products are exact, the sums fp32.
+//
+// Packing is bound by memory (3 bytes an element: 8192 x 8192 42 us, 4.8 TB/s;
+// 48 with 16-byte stores of each lane's own columns, which leave lines half
+// written), unpacking too (40 us).  The gradient: kepttile.hpp; 8192^3 to fp32
+// 810 us, 1.36 PFLOP/s.
 #include <hip/hip_runtime.h>
 
 #include <math.h>

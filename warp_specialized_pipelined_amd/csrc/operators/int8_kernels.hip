@@ -6,7 +6,11 @@
 //
 // The kernels are the scaled product's (scaled_tiles.hpp), with two
 // v_mfma_i32_32x32x32_i8 in place of one 32x32x64 e4m3 instruction: the same
-// bytes of K a lane, the same fragments, the same cycles.
+// bytes of K a lane, the same fragments.  Few rows are bound by b's bytes (1 x
+// 8192 x 8192: 12.3 us, 5.5 TB/s; 33 x 16384 x 8192: 33 us, 4.1 TB/s, and 30
+// where b's stride is 8320: a stride of a power of two sends a stage's rows to
+// few channels), many by the matrix instructions (8192 x 8192 x 16384: 810 us,
+// 2.7 POP/s; 4000 x 3000 x 5000, one round of 252 tiles: 64 us).
 #include "scaled_tiles.hpp"
 
 namespace migemm {

@@ -1,9 +1,9 @@
 // kepttile.hpp -- tiles of dw = dy^T x~, x~ the kept activations (e4m3 codes, a
 // power of two for each 32 tokens of a column), on the bf16 matrix instructions.
 //
-// A workgroup of 4 waves takes a TM x TN tile (rows: columns of dy; columns:
-// those of x~), each wave a TM/2 x TN/2 quarter in blocks of 32 x 32.  K are the
-// tokens, 64 to a stage.  In LDS a stage is
+// A workgroup of WM x WN waves takes a TM x TN tile (rows: columns of dy;
+// columns: those of x~), each wave TM/WM x TN/WN of it in blocks of 32 x 32.  K
+// are the tokens, 64 to a stage.  In LDS a stage is
 //   dy:     panels of 64 columns, 64 rows of 128 bytes each, swizzled as the
 //           GEMM's MN-contiguous operands (kernel/mainloop.hpp) and read with
 //           transposing reads;
@@ -18,6 +18,16 @@
 // Codes become bf16 in registers, a v_cvt_scalef32_pk_bf16_fp8 for each pair,
 // which applies the power too: exact, and four of them to a fragment of eight.
 // Half the bytes of a bf16 operand go through memory and LDS.
+//
+// Bound: the matrix instructions, 65 to 70% of the time busy.  With the codes
+// taken for bf16 as they are the loop takes as long, so the conversions hide
+// behind the products; without its loads it takes 15% less (256 x 256, 128
+// stages: 126 us for 145).  The large tiles have eight waves, two a SIMD: one's
+// products run while the other waits at the barrier or for its fragments.  With
+// four, each with twice the blocks and all of a SIMD's registers, 1000^3 in one
+// round of 192 x 256 took 23.3 us for 20.8 and 2048 x 4096 x 11008 186 for 180;
+// the small tiles have their second workgroup for that (128 x 128 with eight
+// waves: slower).
 //
 // The ring has SLOTS >= 3 stages.  An iteration begins behind the barrier that
 // certifies stage d + 1 and frees stage d, whose last k-step is in registers:

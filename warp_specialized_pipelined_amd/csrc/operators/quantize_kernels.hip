@@ -11,7 +11,8 @@
 // exact in one fma, and q0 plus remainder / max |x| is rounded once.
 //
 // Bound: memory (3 bytes an element); a row is read once and stays in registers
-// between its maximum and its codes.
+// between its maximum and its codes.  8192 x 16384: 74 us, 5.4 TB/s; 33 x 8192:
+// 3.5 us, what a launch of any kernel takes.
 #include <hip/hip_runtime.h>
 
 #include "../kernel/gfx950.hpp"
@@ -101,7 +102,9 @@ quantize_fn pick_shape(NormShape s) {
 }  // namespace
 
 // The norm's shapes, but many rows of 8193 to 16384 columns are shared by four
-// waves with eight vectors a lane.
+// waves with eight vectors a lane: a wave has more bytes on their way before
+// the first wait (8192 x 16384: 74 us, 90 with sixteen waves and two vectors).
+// Few rows are better off with more waves.
 NormShape quantize_shape(int64_t rows, int64_t cols) {
   const NormShape s = norm_shape(rows, cols);
   return rows > 256 && s.waves == 16 && s.vectors <= 2 ? NormShape{4, 8} : s;
