@@ -21,7 +21,10 @@
 // registers through both reductions.  8192 x 8192 to e4m3 with a gate: 119 us,
 // 5.1 TB/s; one row of 8192: 4.2 us, two reductions and three waits for memory;
 // backward 8192 x 4096 with everything: 109 us and 5 for the columns' sums, 4.9
-// TB/s.
+// TB/s.  Rows of an odd number of columns have kernels of their own (RowView),
+// which clear the value past the last once all of a row's loads are on their
+// way: 8192 x 3001 98 us backward and 56 forward; 173 and 72 with a branch and
+// a wait at each load, and 104 and 57 with a branch for the row in all kernels.
 #include <hip/hip_runtime.h>
 
 #include "../kernel/gfx950.hpp"
@@ -81,9 +84,10 @@ __device__ __forceinline__ float row_sum(float v, float* buffer, int wave, int l
   return v;
 }
 
-template <int WAVES, int NV, bool GATE, RowType Y>
+template <int WAVES, int NV, bool GATE, RowType Y, bool ODD>
 __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t row, int t, int wave, int lane,
                                                int phase) {
+  typedef RowView<ODD> Row;
   constexpr int kLanes = 64 * WAVES;
   // Two buffers each: a wave that is already at its next row writes the other
   // ones, and cannot come round to these before a barrier between.
@@ -91,11 +95,11 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   __shared__ uint32_t tops[2][WAVES];
   const auto at = [&](int i) { return (i * kLanes + t) * 8; };
   const auto load = [&](u32x4 (&v)[NV], const void* m, int64_t rs) {
-    const RowView from = RowView::in(m, row * rs, a.cols);
+    const Row from = Row::in(m, row * rs, a.cols);
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = from.load(at(i));
   };
-  const RowView pw = RowView::in(a.post_weight, 0, a.post_weight ? a.cols : 0);
+  const Row pw = Row::in(a.post_weight, 0, a.post_weight ? a.cols : 0);
   u32x4 xv[NV], rv[NV], zv[NV], wv[NV];
   load(xv, a.x, a.x_rs);
   if constexpr (GATE) load(zv, a.z, a.z_rs);
@@ -105,6 +109,14 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   // before the first sum, too; else it is read behind it, from the caches.
   u32x4 early = {0, 0, 0, 0};
   if (NV == 1 && a.post_weight) early = pw.load(at(0));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    Row::clear_past(xv[i], at(i), a.cols);
+    if constexpr (GATE) Row::clear_past(zv[i], at(i), a.cols);
+    Row::clear_past(rv[i], at(i), a.cols);
+    Row::clear_past(wv[i], at(i), a.cols);
+  }
+  Row::clear_past(early, at(0), a.cols);
 
   float post = 1.0f;
   if (a.post_weight) {
@@ -118,11 +130,11 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   }
   float h[NV][8], sum = 0.0f;
   uint32_t top = 0;
-  const RowView ho = RowView::out<2>(a.h, row * a.h_rs, a.cols);
+  const Row ho = Row::template out<2>(a.h, row * a.h_rs, a.cols);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     u32x4 pv = early;
-    if (NV > 1 && a.post_weight) pv = pw.load(at(i));
+    if (NV > 1 && a.post_weight) pv = pw.load_cleared(at(i));
     u32x4 o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -148,7 +160,7 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   const float rstd = rsqrtf(row_sum<WAVES>(sum, sums[phase], wave, lane) / (float)a.cols + a.eps);
   if (t == 0) a.rstd[row] = rstd;
   if constexpr (Y == kRowBf16) {
-    const RowView y = RowView::out<2>(a.y, row * a.y_rs, a.cols);
+    const Row y = Row::template out<2>(a.y, row * a.y_rs, a.cols);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       u32x4 o;
@@ -171,7 +183,7 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
     // Rows of values so small that kTop / largest would overflow are lifted.
     const float lift = largest < 0x1p-96f ? 0x1p96f : 1.0f;
     const float inv = largest == 0.0f ? 0.0f : kTop / (largest * lift);
-    const RowView y = RowView::out<1>(a.y, row * a.y_rs, a.cols);
+    const Row y = Row::template out<1>(a.y, row * a.y_rs, a.cols);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float v[8];
@@ -189,7 +201,7 @@ __device__ __forceinline__ void block_norm_row(const BlockNormArgs& a, int64_t r
   }
 }
 
-template <int WAVES, int NV, bool GATE, RowType Y>
+template <int WAVES, int NV, bool GATE, RowType Y, bool ODD>
 __global__ __launch_bounds__(threads_of(WAVES)) void block_norm_forward(BlockNormArgs a) {
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const int t = WAVES == 1 ? lane : (int)threadIdx.x;
@@ -197,13 +209,14 @@ __global__ __launch_bounds__(threads_of(WAVES)) void block_norm_forward(BlockNor
   const int64_t step = (int64_t)gridDim.x * rows_of(WAVES);
   for (int64_t row = (int64_t)blockIdx.x * rows_of(WAVES) + (WAVES == 1 ? wave : 0); row < a.rows;
        row += step, phase ^= 1)
-    block_norm_row<WAVES, NV, GATE, Y>(a, row, t, wave, lane, phase);
+    block_norm_row<WAVES, NV, GATE, Y, ODD>(a, row, t, wave, lane, phase);
 }
 
 // What a lane holds of a row: the gradients that come in, h as it was stored,
 // and the block's output and its gate.
-template <int NV, bool GATE, bool POST>
+template <int NV, bool GATE, bool POST, bool ODD>
 struct BackwardRow {
+  typedef RowView<ODD> Row;
   u32x4 g[NV], h[NV], d[NV], x[GATE || POST ? NV : 1], z[GATE ? NV : 1];
   float rstd, post;
   // (A row past the last: zeros, and nothing is read.)
@@ -211,7 +224,7 @@ struct BackwardRow {
   __device__ __forceinline__ void load(const BlockNormArgs& a, int64_t row, At&& at) {
     const bool in = row < a.rows;
     const auto all = [&](u32x4* v, const void* m, int64_t rs) {
-      const RowView from = RowView::in(m, row * rs, in && m ? a.cols : 0);
+      const Row from = Row::in(m, row * rs, in && m ? a.cols : 0);
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = from.load(at(i));
     };
@@ -223,6 +236,17 @@ struct BackwardRow {
     rstd = in ? a.rstd[row] : 0.0f;
     post = POST && in ? a.post_rstd[row] : 1.0f;
   }
+  template <class At>
+  __device__ __forceinline__ void clear_past(int64_t cols, At&& at) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Row::clear_past(g[i], at(i), cols);
+      Row::clear_past(h[i], at(i), cols);
+      Row::clear_past(d[i], at(i), cols);
+      if constexpr (GATE || POST) Row::clear_past(x[i], at(i), cols);
+      if constexpr (GATE) Row::clear_past(z[i], at(i), cols);
+    }
+  }
 };
 
 // Each walker (a workgroup, or with WAVES = 1 a wave) takes rows walker,
@@ -233,8 +257,9 @@ struct BackwardRow {
 // The workgroup's sums go to its row of the workspace (dw's, then dw_post's);
 // block_norm_sum_partials adds those rows in a fixed order.  One workgroup alone
 // writes the gradients itself.
-template <int WAVES, int NV, bool GATE, bool POST, bool WIDE>
+template <int WAVES, int NV, bool GATE, bool POST, bool WIDE, bool ODD>
 __global__ __launch_bounds__(threads_of(WAVES), WAVES == 16 ? 4 : 2) void block_norm_backward(BlockNormArgs a) {
+  typedef RowView<ODD> Row;
   constexpr int kLanes = 64 * WAVES;
   static_assert(!WIDE || WAVES > 1, "a wave's own sums stay in registers");
   // (WIDE: the weights are read again for each row, from the caches.)
@@ -250,7 +275,7 @@ __global__ __launch_bounds__(threads_of(WAVES), WAVES == 16 ? 4 : 2) void block_
   f32x4* lds = WIDE ? (f32x4*)lds_at(0) : nullptr;
   const auto slot = [&](int which, int i, int half) { return ((which * NV + i) * 2 + half) * kLanes + t; };
 
-  const RowView w = RowView::in(a.weight, 0, a.cols), pw = RowView::in(a.post_weight, 0, POST ? a.cols : 0);
+  const Row w = Row::in(a.weight, 0, a.cols), pw = Row::in(a.post_weight, 0, POST ? a.cols : 0);
   u32x4 wv[NV], pv[POST ? NV : 1];
   float dw[WIDE ? 1 : NV][8], dpw[POST && !WIDE ? NV : 1][8];
 #pragma unroll
@@ -259,8 +284,8 @@ __global__ __launch_bounds__(threads_of(WAVES), WAVES == 16 ? 4 : 2) void block_
 #pragma unroll
       for (int k = 0; k < (POST ? 4 : 2); ++k) lds[slot(k / 2, i, k % 2)] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     } else {
-      if constexpr (!kReload) wv[i] = w.load(at(i));
-      if constexpr (POST && !kReload) pv[i] = pw.load(at(i));
+      if constexpr (!kReload) wv[i] = w.load_cleared(at(i));
+      if constexpr (POST && !kReload) pv[i] = pw.load_cleared(at(i));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dw[i][e] = 0.0f;
@@ -268,19 +293,20 @@ __global__ __launch_bounds__(threads_of(WAVES), WAVES == 16 ? 4 : 2) void block_
       }
     }
   }
-  BackwardRow<NV, GATE, POST> c, next;
+  BackwardRow<NV, GATE, POST, ODD> c, next;
   if constexpr (kAhead) next.load(a, walker, at);
   int phase = 0;
   for (int64_t row = walker; row < a.rows; row += walkers, phase ^= 1) {
     if constexpr (kAhead) c = next;
     else c.load(a, row, at);
     if constexpr (kAhead && !WIDE) next.load(a, row + walkers, at);
+    c.clear_past(a.cols, at);
     // (Pairs of elements are kept apart: all of a row's at once would not fit the
     // registers.)
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if constexpr (kReload) wv[i] = w.load(at(i));
+      if constexpr (kReload) wv[i] = w.load_cleared(at(i));
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -300,14 +326,14 @@ __global__ __launch_bounds__(threads_of(WAVES), WAVES == 16 ? 4 : 2) void block_
     hide(c.h);
     hide(wv);
     if constexpr (POST && !kReload) hide(pv);
-    const RowView dr = RowView::out<2>(a.dr, row * a.dr_rs, a.cols);
-    const RowView dz = RowView::out<2>(a.dz, row * a.dz_rs, a.cols);
-    const RowView dx = RowView::out<2>(a.dx, row * a.dx_rs, a.cols);
+    const Row dr = Row::template out<2>(a.dr, row * a.dr_rs, a.cols);
+    const Row dz = Row::template out<2>(a.dz, row * a.dz_rs, a.cols);
+    const Row dx = Row::template out<2>(a.dx, row * a.dx_rs, a.cols);
     float v[NV][8];
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if constexpr (POST && kReload) pv[i] = pw.load(at(i));
+      if constexpr (POST && kReload) pv[i] = pw.load_cleared(at(i));
       u32x4 o, oz;
       float f[8];
 #pragma unroll
@@ -433,36 +459,42 @@ __global__ __launch_bounds__(GROUPS * COLS) void block_norm_sum_partials(BlockNo
 }
 
 typedef void (*block_norm_fn)(BlockNormArgs);
-template <int WAVES, int NV>
+template <int WAVES, int NV, bool ODD>
 block_norm_fn forward_of(bool gate, int y) {
   if (gate)
-    return y == kRowBf16 ? block_norm_forward<WAVES, NV, true, kRowBf16>
-                         : (y == kRowE4M3 ? block_norm_forward<WAVES, NV, true, kRowE4M3>
-                                          : block_norm_forward<WAVES, NV, true, kRowInt8>);
-  return y == kRowBf16 ? block_norm_forward<WAVES, NV, false, kRowBf16>
-                       : (y == kRowE4M3 ? block_norm_forward<WAVES, NV, false, kRowE4M3>
-                                        : block_norm_forward<WAVES, NV, false, kRowInt8>);
+    return y == kRowBf16 ? block_norm_forward<WAVES, NV, true, kRowBf16, ODD>
+                         : (y == kRowE4M3 ? block_norm_forward<WAVES, NV, true, kRowE4M3, ODD>
+                                          : block_norm_forward<WAVES, NV, true, kRowInt8, ODD>);
+  return y == kRowBf16 ? block_norm_forward<WAVES, NV, false, kRowBf16, ODD>
+                       : (y == kRowE4M3 ? block_norm_forward<WAVES, NV, false, kRowE4M3, ODD>
+                                        : block_norm_forward<WAVES, NV, false, kRowInt8, ODD>);
 }
-template <int WAVES, int NV, bool WIDE>
+template <int WAVES, int NV, bool WIDE, bool ODD>
 block_norm_fn backward_of(bool gate, bool post) {
   if (gate)
-    return post ? block_norm_backward<WAVES, NV, true, true, WIDE> : block_norm_backward<WAVES, NV, true, false, WIDE>;
-  return post ? block_norm_backward<WAVES, NV, false, true, WIDE> : block_norm_backward<WAVES, NV, false, false, WIDE>;
+    return post ? block_norm_backward<WAVES, NV, true, true, WIDE, ODD>
+                : block_norm_backward<WAVES, NV, true, false, WIDE, ODD>;
+  return post ? block_norm_backward<WAVES, NV, false, true, WIDE, ODD>
+              : block_norm_backward<WAVES, NV, false, false, WIDE, ODD>;
 }
+template <bool ODD>
 block_norm_fn forward_pick(NormShape s, bool gate, int y) {
-  if (s.waves == 16) return forward_of<16, 1>(gate, y);
-  if (s.waves == 8) return forward_of<8, 4>(gate, y);
+  if (s.waves == 16) return forward_of<16, 1, ODD>(gate, y);
+  if (s.waves == 8) return forward_of<8, 4, ODD>(gate, y);
   if (s.waves == 4)
-    return s.vectors == 1 ? forward_of<4, 1>(gate, y)
-                          : (s.vectors == 2 ? forward_of<4, 2>(gate, y) : forward_of<4, 4>(gate, y));
-  return s.vectors == 1 ? forward_of<1, 1>(gate, y)
-                        : (s.vectors == 2 ? forward_of<1, 2>(gate, y) : forward_of<1, 4>(gate, y));
+    return s.vectors == 1 ? forward_of<4, 1, ODD>(gate, y)
+                          : (s.vectors == 2 ? forward_of<4, 2, ODD>(gate, y) : forward_of<4, 4, ODD>(gate, y));
+  return s.vectors == 1 ? forward_of<1, 1, ODD>(gate, y)
+                        : (s.vectors == 2 ? forward_of<1, 2, ODD>(gate, y) : forward_of<1, 4, ODD>(gate, y));
 }
+template <bool ODD>
 block_norm_fn backward_pick(NormShape s, bool gate, bool post) {
-  if (s.waves == 16) return backward_of<16, 1, false>(gate, post);
-  if (s.waves == 8) return s.vectors == 2 ? backward_of<8, 2, false>(gate, post) : backward_of<8, 4, true>(gate, post);
-  if (s.waves == 4) return s.vectors == 1 ? backward_of<4, 1, false>(gate, post) : backward_of<4, 2, false>(gate, post);
-  return s.vectors == 1 ? backward_of<1, 1, false>(gate, post) : backward_of<1, 2, false>(gate, post);
+  if (s.waves == 16) return backward_of<16, 1, false, ODD>(gate, post);
+  if (s.waves == 8)
+    return s.vectors == 2 ? backward_of<8, 2, false, ODD>(gate, post) : backward_of<8, 4, true, ODD>(gate, post);
+  if (s.waves == 4)
+    return s.vectors == 1 ? backward_of<4, 1, false, ODD>(gate, post) : backward_of<4, 2, false, ODD>(gate, post);
+  return s.vectors == 1 ? backward_of<1, 1, false, ODD>(gate, post) : backward_of<1, 2, false, ODD>(gate, post);
 }
 // LDS of the wide backward kernel: both weights' sums of 16384 columns.
 constexpr int kWideLds = 2 * 4 * (int)kBlockNormMaxCols;
@@ -500,16 +532,19 @@ int64_t block_norm_partial_rows(int64_t rows, int64_t cols, int cu_count) {
 hipError_t prepare_block_norm() {
   for (bool gate : {false, true})
     for (bool post : {false, true}) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(backward_of<8, 4, true>(gate, post)),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, kWideLds);
-      if (e != hipSuccess) return e;
+      for (block_norm_fn f : {backward_of<8, 4, true, false>(gate, post), backward_of<8, 4, true, true>(gate, post)}) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kWideLds);
+        if (e != hipSuccess) return e;
+      }
     }
   return hipSuccess;
 }
 
 hipError_t launch_block_norm_forward(const BlockNormArgs& a, int y_type, hipStream_t stream) {
   const NormShape s = block_norm_forward_shape(a.rows, a.cols);
-  const block_norm_fn f = forward_pick(s, a.z != nullptr, y_type);
+  const bool gate = a.z != nullptr;
+  const block_norm_fn f = a.cols & 1 ? forward_pick<true>(s, gate, y_type) : forward_pick<false>(s, gate, y_type);
   int64_t grid = (a.rows + rows_of(s.waves) - 1) / rows_of(s.waves);
   if (grid > (1 << 20)) grid = 1 << 20;  // a launch holds fewer than 2^32 threads
   hipLaunchKernelGGL(f, dim3((uint32_t)grid), dim3(threads_of(s.waves)), 0, stream, a);
@@ -520,7 +555,8 @@ hipError_t launch_block_norm_backward(const BlockNormArgs& a, hipStream_t stream
   const NormShape s = block_norm_backward_shape(a.rows, a.cols);
   const bool post = a.dpost_weight != nullptr;
   if (a.partial_rows > 0) {
-    const block_norm_fn f = backward_pick(s, a.dz != nullptr, post);
+    const bool gate = a.dz != nullptr;
+    const block_norm_fn f = a.cols & 1 ? backward_pick<true>(s, gate, post) : backward_pick<false>(s, gate, post);
     hipLaunchKernelGGL(f, dim3((uint32_t)a.partial_rows), dim3(threads_of(s.waves)), s.vectors == 4 ? kWideLds : 0, stream,
                        a);
     const hipError_t e = hipGetLastError();

@@ -59,8 +59,9 @@ __device__ __forceinline__ void store8_bytes(unsigned char* row, int64_t c, int6
 }
 // A row through a buffer resource over its columns: what a lane has past them
 // reads as zeros and is not written, without branches (range checks work on
-// dwords; the element or bytes in a last, partial one are seen to apart).
-// Wave-uniform.
+// dwords; the element or bytes in a last, partial one are seen to apart: ODD,
+// with an odd number of columns).  Wave-uniform.
+template <bool ODD>
 struct RowView {
   __amdgpu_buffer_rsrc_t rsrc;
   int cols;
@@ -73,19 +74,26 @@ struct RowView {
   static __device__ __forceinline__ RowView out(void* m, int64_t elements, int64_t cols) {
     return {make_rsrc(static_cast<unsigned char*>(m) + elements * ES, (uint32_t)(cols * ES)), (int)cols};
   }
-  // Eight bf16 at column c.
+  // Eight bf16 at column c; with ODD the one past the last column holds anything
+  // until it is cleared, which waits for the load.
   __device__ __forceinline__ u32x4 load(int c) const {
-    u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, 2 * c, 0, 0));
-    if (cols & 1) {
-      const int last = (cols - c) >> 1;  // the dword that holds the last column
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, 2 * c, 0, 0));
+  }
+  static __device__ __forceinline__ void clear_past(u32x4& v, int c, int64_t cols) {
+    if constexpr (ODD) {
+      const int last = ((int)cols - c) >> 1;  // the dword that holds the last column
 #pragma unroll
       for (int w = 0; w < 4; ++w) v[w] = w == last ? v[w] & 0xFFFFu : v[w];
     }
+  }
+  __device__ __forceinline__ u32x4 load_cleared(int c) const {
+    u32x4 v = load(c);
+    clear_past(v, c, cols);
     return v;
   }
   __device__ __forceinline__ void store(int c, u32x4 v) const {
     __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, 2 * c, 0, 0);
-    if (cols & 1) {
+    if constexpr (ODD) {
 #pragma unroll
       for (int w = 0; w < 4; ++w)
         if (w == (cols - c) >> 1) __builtin_amdgcn_raw_buffer_store_b16((unsigned short)v[w], rsrc, 2 * (c + 2 * w), 0, 0);
