@@ -479,7 +479,10 @@ def test_runs_agree_on_streams_and_in_a_graph(y_type):
 @pytest.mark.parametrize("rows,cols,forward,backward", [
     (5, 512, (1, 1), (1, 1)), (2000, 500, (1, 1), (1, 1)), (300, 1001, (1, 2), (1, 2)), (300, 2000, (1, 4), (4, 1)),
     (5, 2048, (4, 1), (4, 1)), (300, 4001, (4, 2), (4, 2)), (300, 8190, (4, 4), (8, 2)), (3, 8001, (16, 1), (16, 1)),
-    (40, 16383, (8, 4), (8, 4)), (700, 12001, (8, 4), (8, 4))])
+    (40, 16383, (8, 4), (8, 4)), (700, 12001, (8, 4), (8, 4)),
+    # (even and odd numbers of columns have kernels of their own)
+    (5, 511, (1, 1), (1, 1)), (300, 1000, (1, 2), (1, 2)), (300, 1999, (1, 4), (4, 1)), (5, 2047, (4, 1), (4, 1)),
+    (300, 4000, (4, 2), (4, 2)), (300, 8191, (4, 4), (8, 2)), (3, 8000, (16, 1), (16, 1)), (40, 16382, (8, 4), (8, 4))])
 def test_kernels_that_a_plan_chooses(rows, cols, forward, backward):
     for gate, post in ((True, True), (False, True), (True, False), (False, False)):
         p = Block(rows, cols, post=post, gate=gate, seed=rows + cols)
