@@ -18,12 +18,12 @@
 //
 // Bound: memory (forward 7 bytes an element to codes, with a gate 9; backward
 // with everything 16).  A row is read once, 16 bytes a lane, and stays in
-// registers through both reductions.  8192 x 8192 to e4m3 with a gate: 119 us,
-// 5.1 TB/s; one row of 8192: 4.2 us, two reductions and three waits for memory;
+// registers through both reductions.  8192 x 8192 to e4m3 with a gate: 115 us,
+// 5.3 TB/s; one row of 8192: 4.2 us, two reductions and three waits for memory;
 // backward 8192 x 4096 with everything: 109 us and 5 for the columns' sums, 4.9
 // TB/s.  Rows of an odd number of columns have kernels of their own (RowView),
 // which clear the value past the last once all of a row's loads are on their
-// way: 8192 x 3001 98 us backward and 56 forward; 173 and 72 with a branch and
+// way: 8192 x 3001 96 us backward and 56 forward; 173 and 72 with a branch and
 // a wait at each load, and 104 and 57 with a branch for the row in all kernels.
 #include <hip/hip_runtime.h>
 
@@ -226,7 +226,10 @@ struct BackwardRow {
     const auto all = [&](u32x4* v, const void* m, int64_t rs) {
       const Row from = Row::in(m, row * rs, in && m ? a.cols : 0);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = from.load(at(i));
+      for (int i = 0; i < NV; ++i) {
+        v[i] = from.load(at(i));
+        apart();  // (in this order: 8192 x 5000 178 us without, 160 with this and the stores kept in theirs)
+      }
     };
     all(g, a.dy, a.dy_rs);
     all(h, a.h, a.h_rs);
@@ -367,6 +370,7 @@ __global__ __launch_bounds__(threads_of(WAVES), WAVES == 16 ? 4 : 2) void block_
       }
       dr.store(at(i), o);
       if constexpr (GATE) dz.store(at(i), oz);
+      apart();
       if constexpr (POST && WIDE) {
         lds[slot(1, i, 0)] += f32x4{f[0], f[1], f[2], f[3]};
         lds[slot(1, i, 1)] += f32x4{f[4], f[5], f[6], f[7]};
