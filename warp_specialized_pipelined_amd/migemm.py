@@ -605,7 +605,6 @@ class _OperatorPlan:
         if st != MIGEMM_OK:
             raise MigemmError(st, f"gemm_{self.kind}_plan_create")
         self.handle = h.value
-        self._info = None
 
     @property
     def workspace_size(self) -> int:
@@ -613,14 +612,11 @@ class _OperatorPlan:
 
     @property
     def info(self):
-        """The kernels the plan has chosen (a plan never changes: asked once)."""
-        if self._info is not None:
-            return self._info
+        """The kernels the plan has chosen."""
         info = self.info_type()
         st = getattr(load(), f"gemm_{self.kind}_plan_get_info")(self.handle, ctypes.byref(info))
         if st != MIGEMM_OK:
             raise MigemmError(st, f"gemm_{self.kind}_plan_get_info")
-        self._info = info
         return info
 
     def __del__(self):
