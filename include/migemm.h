@@ -562,7 +562,9 @@ int gemm_vocab_loss_run_backward(const migemm_vocab_loss_plan* plan, const void*
  * codes from -128 to 127; d is M x N bf16.  The sum is int32 and exact, then
  * rounded to fp32 (2^-24 of it); scales and bias are fp32, and the result is
  * rounded to bf16 once.  K is at most 131071 (more: UNSUPPORTED), so that no
- * sum leaves int32.  Otherwise sizes, strides and the workspace are as the
+ * sum leaves int32.  The factors are taken in the order sum, a_scale, b_scale,
+ * each product in fp32: one that passes 3e38 on the way is infinite, whatever
+ * stands behind it.  Otherwise sizes, strides and the workspace are as the
  * scaled product's. */
 typedef struct migemm_int8_desc {
   int64_t M, N, K;
@@ -639,7 +641,8 @@ int gemm_quantize_run(const migemm_quantize_plan* plan, const void* x, void* q, 
  * where it is stored; rstd, y and scale come from it before that.  A row of
  * zeros gets scale 0 and codes 0.  A row of h with an infinity or a NaN has a
  * NaN or infinite scale with e4m3, and with int8 a NaN scale and codes 0: its
- * products hold no number.
+ * products hold no number.  8-bit rows are made of h * weight in fp32: a row
+ * where that passes 3e38 counts as one with an infinity.
  * Gradients, with h as it was stored, n = h * rstd, s = sigmoid(z), p = x *
  * post_rstd, g = dy:
  *   d = dh + rstd * (g * weight - n * mean(g * weight * n))
