@@ -15,7 +15,8 @@
 // Packing is bound by memory (3 bytes an element: 8192 x 8192 42 us, 4.8 TB/s;
 // 48 with 16-byte stores of each lane's own columns, which leave lines half
 // written), unpacking too (40 us).  The gradient: kepttile.hpp; 8192^3 to fp32
-// 810 us, 1.36 PFLOP/s.
+// 810 us, 1.36 PFLOP/s, and 880 added to what is there (2048 x 4096 x 11008: 169
+// and 228), which each tile reads behind its products.
 #include <hip/hip_runtime.h>
 
 #include <math.h>

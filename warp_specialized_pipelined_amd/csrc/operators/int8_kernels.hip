@@ -6,11 +6,13 @@
 //
 // The kernels are the scaled product's (scaled_tiles.hpp), with two
 // v_mfma_i32_32x32x32_i8 in place of one 32x32x64 e4m3 instruction: the same
-// bytes of K a lane, the same fragments.  Few rows are bound by b's bytes (1 x
-// 8192 x 8192: 12.3 us, 5.5 TB/s; 33 x 16384 x 8192: 33 us, 4.1 TB/s, and 30
-// where b's stride is 8320: a stride of a power of two sends a stage's rows to
-// few channels), many by the matrix instructions (8192 x 8192 x 16384: 810 us,
-// 2.7 POP/s; 4000 x 3000 x 5000, one round of 252 tiles: 64 us).
+// bytes of K a lane, the same fragments.  Few rows are bound by b's bytes. 1 x
+// 8192 x 8192 takes 14.9 us with b from memory, 4.5 TB/s, and 12.3 with two b's
+// in turn, which the 256 MB last-level cache holds; 33 x 16384 x 8192 33 us (4.1
+// TB/s) and 27, and from memory 30 where b's stride is 8320: one of a power of
+// two sends a stage's rows to few channels.  Many rows are bound by the matrix
+// instructions (8192 x 8192 x 16384: 800 to 860 us from card to card, 2.6 to 2.7
+// POP/s; 4000 x 3000 x 5000, one round of 252 tiles: 64 to 68 us).
 #include "scaled_tiles.hpp"
 
 namespace migemm {
@@ -39,7 +41,13 @@ const CostModel kCost = {kLast, 10.4e6, 0.25, 1.1, true, 7.5, 11e6};
 // 1 to 16384 rows, 64 to 16384 columns and K of 64 to 16384 and 965 of up to 200
 // rows, 512 to 17000 columns and K of 512 to 16384, each timed with every kernel
 // and up to 16 splits.  What it picks is 1.7% and 2.2% slower than the fastest
-// of them on average (4.7% and 5.9% with the e4m3 product's figures).
+// of them on average (4.7% and 5.9% with the e4m3 product's figures).  Each was
+// timed on two sets of operands in turn, so that operands of up to 128 MB came
+// from the last-level cache, whose rate kCost's memory rate is (10.4 TB/s; a copy
+// moves 5.2).  From memory what it picks takes 3 to 24% longer (33 x 8192 x 8192
+// 19.3 and 21.1 us, 64 x 11008 x 4096 15.0 and 17.4, 300 x 2000 x 4096 15.0 and
+// 15.6, 128 x 8192 x 8192 26.4 and 27.6); whether another kernel would then be
+// the fastest was not measured.
 ScaledChoice choose_int8(int64_t M, int64_t N, int64_t K, int cu_count) {
   return cheapest_variant(kCost, kVariants, M, N, K, cu_count);
 }

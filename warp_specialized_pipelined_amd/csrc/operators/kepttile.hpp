@@ -19,9 +19,12 @@
 // which applies the power too: exact, and four of them to a fragment of eight.
 // Half the bytes of a bf16 operand go through memory and LDS.
 //
-// Bound: the matrix instructions, 65 to 70% of the time busy.  With the codes
-// taken for bf16 as they are the loop takes as long, so the conversions hide
-// behind the products; without its loads it takes 15% less (256 x 256, 128
+// Bound: the matrix instructions, busy in 73% of the cycles of 8192^3, at a clock
+// that the board's power limit holds at 1.55 to 1.85 GHz.  Tiles that fill their
+// rounds poorly and have few stages leave them idle: 2048 x 4096 x 11008 (928
+// tiles of 32 stages, 3.6 rounds) 50%, 1001 x 2000 x 5000 (216 of 16) 29%.  With
+// the codes taken for bf16 as they are the loop takes as long, so the conversions
+// hide behind the products; without its loads it takes 15% less (256 x 256, 128
 // stages: 126 us for 145).  The large tiles have eight waves, two a SIMD: one's
 // products run while the other waits at the barrier or for its fragments.  With
 // four, each with twice the blocks and all of a SIMD's registers, 1000^3 in one

@@ -1,5 +1,5 @@
 // operators.h -- internal interface between the operators' plan layer
-// (operators_api.cpp) and their kernels: argument blocks and launches.
+// (operators_api.cpp, block_api.cpp) and their kernels: argument blocks and launches.
 #pragma once
 
 #include <hip/hip_runtime.h>
